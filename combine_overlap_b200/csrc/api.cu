@@ -201,6 +201,31 @@ int choose_variant(int T, int f, int E, int k, unsigned flags) {
 inline int bands_per_tile(int V) { return V == 1 ? 1 : 2; }
 inline int ctas_per_tile(int V) { return V == 2 ? 2 : 1; }
 
+inline bool ok_dtype(int t) { return t == MOE_DTYPE_BF16 || t == MOE_DTYPE_F32; }
+
+// Sizes of a linear layer: any M, K, N whose matrices stay under 2^40 elements.
+moe_status check_linear_shape(int M, int K, int N) {
+  if (M < 1 || K < 1 || N < 1) return MOE_ERR_INVALID;
+  const long long lim = 1LL << 40;
+  if ((long long)M * K >= lim || (long long)K * N >= lim || (long long)M * N >= lim) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// The router's options, checked against (E, k) and with their defaults filled in.
+moe_status check_router(const moe_router* q, int E, int k, RouterArgs* r) {
+  if (!q) return MOE_ERR_INVALID;
+  const int G = q->n_groups == 0 ? 1 : q->n_groups;
+  const int kg = q->topk_groups == 0 ? G : q->topk_groups;
+  if ((q->score != MOE_SCORE_SOFTMAX && q->score != MOE_SCORE_SIGMOID) || !ok_opt(q->bias))
+    return MOE_ERR_INVALID;
+  if (q->group_score != MOE_GROUP_MAX && q->group_score != MOE_GROUP_TOP2) return MOE_ERR_INVALID;
+  if (G < 1 || kg < 1 || kg > G || E % G != 0 || k > (long long)kg * (E / G)) return MOE_ERR_INVALID;
+  if (G > 32) return MOE_ERR_UNSUPPORTED;
+  if (!(q->scale - q->scale == 0.0f)) return MOE_ERR_INVALID;   // infinite or NaN
+  *r = {q->score, q->bias, G, kg, q->group_score == MOE_GROUP_TOP2, q->renorm != 0, q->scale};
+  return MOE_OK;
+}
+
 #define MOE_TRY(expr)                                   \
   do {                                                  \
     cudaError_t e_ = (expr);                            \
@@ -339,8 +364,11 @@ moe_status moe_combine(const void* y, const int32_t* row_of, const float* topk_g
                                     static_cast<cudaStream_t>(stream)));
 }
 
-moe_status moe_layer_forward(const moe_layer_args* args, moe_mode mode, void* ws, size_t ws_bytes,
-                             void* stream) {
+}  // extern "C"
+
+// moe_layer_forward, and with a router moe_layer_forward_scored.
+static moe_status layer_forward(const moe_layer_args* args, const RouterArgs* router, moe_mode mode,
+                                void* ws, size_t ws_bytes, void* stream) {
   if (!args) return MOE_ERR_INVALID;
   const moe_layer_args& A = *args;
   moe_status s = check_shape(A.T, A.d, A.f, A.E, A.k);
@@ -386,7 +414,11 @@ moe_status moe_layer_forward(const moe_layer_args* args, moe_mode mode, void* ws
   const int T = A.T, d = A.d, f = A.f, E = A.E, k = A.k, R = T * k;
   const int mgb = A.mgb > 0 ? A.mgb : 1;
   const int nblk = route_blocks(T);
-  MOE_TRY(launch_route(A.logits, T, E, k, w.topk_idx, w.topk_gate, w.blk_hist, w.arrive, w.ready_q, st));
+  if (router)
+    MOE_TRY(launch_route_scored(A.logits, T, E, k, *router, w.topk_idx, w.topk_gate, w.blk_hist, w.arrive,
+                                w.ready_q, st));
+  else
+    MOE_TRY(launch_route(A.logits, T, E, k, w.topk_idx, w.topk_gate, w.blk_hist, w.arrive, w.ready_q, st));
   const int join = (A.flags & MOE_SCHED_NO_JOIN) ? 0 : 1;
   // with side warps no SM is a dedicated consumer unless the caller asks for some
   const int consumer_hint = (side && A.consumer_sms == 0) ? -1 : A.consumer_sms;
@@ -442,6 +474,118 @@ moe_status moe_layer_forward(const moe_layer_args* args, moe_mode mode, void* ws
     MOE_TRY(launch_combine(w.y, w.row_of, w.topk_gate, T, d, k, a.out, nsm, st));
   }
   return MOE_OK;
+}
+
+extern "C" {
+
+moe_status moe_layer_forward(const moe_layer_args* args, moe_mode mode, void* ws, size_t ws_bytes,
+                             void* stream) {
+  return layer_forward(args, nullptr, mode, ws, ws_bytes, stream);
+}
+
+moe_status moe_layer_forward_scored(const moe_layer_args* args, const moe_router* router, moe_mode mode,
+                                    void* ws, size_t ws_bytes, void* stream) {
+  if (!args || !router) return MOE_ERR_INVALID;
+  moe_status s = check_route_shape(args->T, args->E, args->k);
+  if (s != MOE_OK) return s;
+  RouterArgs r;
+  s = check_router(router, args->E, args->k, &r);
+  if (s != MOE_OK) return s;
+  return layer_forward(args, &r, mode, ws, ws_bytes, stream);
+}
+
+moe_status moe_route_scored(const float* logits, int T, int E, int k, const moe_router* router,
+                            int32_t* topk_idx, float* topk_gate, int32_t* counts, void* ws,
+                            size_t ws_bytes, void* stream) {
+  moe_status s = check_route_shape(T, E, k);
+  if (s != MOE_OK) return s;
+  RouterArgs r;
+  s = check_router(router, E, k, &r);
+  if (s != MOE_OK) return s;
+  if (!ok_ptr(logits) || !ok_ptr(topk_idx) || !ok_ptr(topk_gate) || !ok_opt(counts))
+    return MOE_ERR_INVALID;
+  int32_t* blk_hist = nullptr;
+  if (counts) {
+    const Layout L = layout(T, BN2, BN1, E, k);
+    if (!ws || !aligned16(ws) || ws_bytes < L.routing_end) return MOE_ERR_WORKSPACE;
+    blk_hist = at<int32_t>(ws, L.blk_hist);
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  MOE_TRY(launch_route_scored(logits, T, E, k, r, topk_idx, topk_gate, blk_hist, nullptr, nullptr, st));
+  if (counts) MOE_TRY(launch_colsum(blk_hist, route_blocks(T), E, counts, st));
+  return MOE_OK;
+}
+
+moe_status moe_route_scored_backward(const float* dgate, const float* logits, const int32_t* topk_idx,
+                                     int T, int E, int k, const moe_router* router, float* dlogits,
+                                     void* stream) {
+  moe_status s = check_route_shape(T, E, k);
+  if (s != MOE_OK) return s;
+  RouterArgs r;
+  s = check_router(router, E, k, &r);
+  if (s != MOE_OK) return s;
+  if (!ok_ptr(dgate) || !ok_ptr(logits) || !ok_ptr(topk_idx) || !ok_ptr(dlogits)) return MOE_ERR_INVALID;
+  const int nsm = device_sms();
+  if (nsm <= 0) return cuda_fail(cudaErrorInvalidDevice);
+  return cuda_status(launch_route_scored_bwd(dgate, logits, topk_idx, T, E, k, r, dlogits, nsm,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_combine_backward(const void* dout, const void* y, const int32_t* row_of,
+                                const float* topk_gate, int T, int d, int k, void* dy, float* dgate,
+                                void* stream) {
+  if (T < 1 || d < 1 || k < 1) return MOE_ERR_INVALID;
+  if (k > MAX_K || d % 8 != 0 || (long long)T * k > (1LL << 30)) return MOE_ERR_UNSUPPORTED;
+  if (!ok_ptr(dout) || !ok_ptr(y) || !ok_ptr(row_of) || !ok_ptr(topk_gate) || !ok_opt(dy) || !ok_ptr(dgate))
+    return MOE_ERR_INVALID;
+  const int nsm = device_sms();
+  if (nsm <= 0) return cuda_fail(cudaErrorInvalidDevice);
+  return cuda_status(launch_combine_bwd(static_cast<const __nv_bfloat16*>(dout),
+                                        static_cast<const __nv_bfloat16*>(y), row_of, topk_gate, T, d, k,
+                                        static_cast<__nv_bfloat16*>(dy), dgate, nsm,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_linear_workspace_size(int M, int K, int N) {
+  return check_linear_shape(M, K, N) == MOE_OK ? linear_ws_bytes(M, K, N) : (size_t)-1;
+}
+
+size_t moe_linear_backward_workspace_size(int M, int K, int N) {
+  return check_linear_shape(M, K, N) == MOE_OK ? linear_bwd_ws_bytes(M, K, N) : (size_t)-1;
+}
+
+moe_status moe_linear(const moe_linear_args* args, void* ws, size_t ws_bytes, void* stream) {
+  if (!args) return MOE_ERR_INVALID;
+  const moe_linear_args& A = *args;
+  moe_status s = check_linear_shape(A.M, A.K, A.N);
+  if (s != MOE_OK) return s;
+  if (A.act < MOE_ACT_NONE || A.act > MOE_ACT_GELU || !ok_dtype(A.out_dtype)) return MOE_ERR_INVALID;
+  if (!ok_ptr(A.x) || !ok_ptr(A.W) || !ok_opt(A.bias) || !ok_opt(A.residual) || !ok_ptr(A.out) ||
+      !ok_opt(A.pre))
+    return MOE_ERR_INVALID;
+  const size_t need = linear_ws_bytes(A.M, A.K, A.N);
+  if (need && (!ws || !aligned16(ws) || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  LinearArgs a = {A.M, A.K, A.N, A.x, A.W, {A.bias, A.residual, A.act, A.out_dtype, A.out, A.pre}};
+  return cuda_status(launch_linear(a, ws, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_linear_backward(const moe_linear_bwd_args* args, void* ws, size_t ws_bytes, void* stream) {
+  if (!args) return MOE_ERR_INVALID;
+  const moe_linear_bwd_args& A = *args;
+  moe_status s = check_linear_shape(A.M, A.K, A.N);
+  if (s != MOE_OK) return s;
+  if (A.act < MOE_ACT_NONE || A.act > MOE_ACT_GELU || !ok_dtype(A.dout_dtype) || !ok_dtype(A.dW_dtype))
+    return MOE_ERR_INVALID;
+  if (!ok_ptr(A.dout) || !ok_opt(A.dx) || !ok_opt(A.dW) || !ok_opt(A.dbias) || !ok_opt(A.x) ||
+      !ok_opt(A.W) || !ok_opt(A.pre))
+    return MOE_ERR_INVALID;
+  if ((A.dx && !A.W) || (A.dW && !A.x) || (A.act != MOE_ACT_NONE && !A.pre)) return MOE_ERR_INVALID;
+  if (!A.dx && !A.dW && !A.dbias) return MOE_ERR_INVALID;
+  const size_t need = linear_bwd_ws_bytes(A.M, A.K, A.N);
+  if (!ws || !aligned16(ws) || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  LinearBwdArgs a = {A.M, A.K, A.N, A.dout, A.x, A.W, A.act ? A.pre : nullptr, A.act, A.dout_dtype,
+                     A.dW_dtype, A.dx, A.dW, A.dbias};
+  return cuda_status(launch_linear_bwd(a, ws, static_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_ep_owner_workspace_size(int N, int d, int f, int El, int W) {

@@ -115,6 +115,53 @@ struct FfnArgs {
   uint32_t* ep_home_arrive[MAX_W];  // [T_home] arrival words of each home rank
 };
 
+// route_scored.cu
+struct RouterArgs {
+  int score;                     // 0 softmax over all experts, 1 sigmoid
+  const float* bias;             // [E] selection bias, or null
+  int n_groups, topk_groups;     // topk_groups == n_groups: no limit
+  int group_top2;
+  int renorm;
+  float scale;
+};
+cudaError_t launch_route_scored(const float* logits, int T, int E, int k, const RouterArgs& r,
+                                int32_t* topk_idx, float* topk_gate, int32_t* blk_hist_or_null,
+                                uint32_t* arrive_or_null, uint32_t* ready_q_or_null, cudaStream_t s);
+cudaError_t launch_route_scored_bwd(const float* dgate, const float* logits, const int32_t* topk_idx,
+                                    int T, int E, int k, const RouterArgs& r, float* dlogits,
+                                    int num_sms, cudaStream_t s);
+
+// combine_bwd.cu
+cudaError_t launch_combine_bwd(const __nv_bfloat16* dout, const __nv_bfloat16* y, const int32_t* row_of,
+                               const float* gate, int T, int d, int k, __nv_bfloat16* dy_or_null,
+                               float* dgate, int num_sms, cudaStream_t s);
+
+// linear.cu
+struct LinearEpi {
+  const float* bias;             // [N] or null
+  const void* residual;          // [M][N] of the output's type, or null
+  int act;                       // moe_act
+  int out_f32;                   // output and residual fp32 instead of bf16
+  void* out;                     // [M][N]
+  void* pre;                     // [M][N] bf16 pre-activation, or null
+};
+struct LinearArgs {
+  int M, K, N;
+  const void* x;                 // [M][K] bf16
+  const void* W;                 // [K][N] bf16
+  LinearEpi ep;
+};
+struct LinearBwdArgs {
+  int M, K, N;
+  const void* dout; const void* x; const void* W; const void* pre;
+  int act, dout_f32, dW_f32;
+  void* dx; void* dW; float* dbias;   // each may be null
+};
+size_t linear_ws_bytes(int M, int K, int N);
+size_t linear_bwd_ws_bytes(int M, int K, int N);
+cudaError_t launch_linear(const LinearArgs& a, void* ws, cudaStream_t s);
+cudaError_t launch_linear_bwd(const LinearBwdArgs& a, void* ws, cudaStream_t s);
+
 size_t ffn_smem_bytes();
 // CTAs the persistent kernel runs with for tile variant V; also sets the
 // kernel's shared-memory attribute for the current device.

@@ -42,6 +42,12 @@ SCHED_EXP_SILU = 0x4000
 SCHED_GATHER_LSU = 0x8000
 
 
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+GROUP_MAX, GROUP_TOP2 = 0, 1
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU = range(4)
+DTYPE_BF16, DTYPE_F32 = 0, 1
+
+
 class MoEError(RuntimeError):
     def __init__(self, code: int, what: str):
         self.code = code
@@ -83,6 +89,33 @@ class EpOwnerArgs(ctypes.Structure):
     ]
 
 
+class RouterArgs(ctypes.Structure):
+    _fields_ = [
+        ("score", ctypes.c_int), ("bias", ctypes.c_void_p),
+        ("n_groups", ctypes.c_int), ("topk_groups", ctypes.c_int), ("group_score", ctypes.c_int),
+        ("renorm", ctypes.c_int), ("scale", ctypes.c_float),
+    ]
+
+
+class LinearArgs(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int), ("K", ctypes.c_int), ("N", ctypes.c_int),
+        ("x", ctypes.c_void_p), ("W", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+        ("residual", ctypes.c_void_p), ("act", ctypes.c_int), ("out_dtype", ctypes.c_int),
+        ("out", ctypes.c_void_p), ("pre", ctypes.c_void_p),
+    ]
+
+
+class LinearBwdArgs(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int), ("K", ctypes.c_int), ("N", ctypes.c_int),
+        ("dout", ctypes.c_void_p), ("x", ctypes.c_void_p), ("W", ctypes.c_void_p),
+        ("pre", ctypes.c_void_p), ("act", ctypes.c_int), ("dout_dtype", ctypes.c_int),
+        ("dW_dtype", ctypes.c_int), ("dx", ctypes.c_void_p), ("dW", ctypes.c_void_p),
+        ("dbias", ctypes.c_void_p),
+    ]
+
+
 _P, _I, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 _lib.moe_workspace_size.argtypes = [_I, _I, _I, _I, _I]
 _lib.moe_workspace_size.restype = _S
@@ -116,6 +149,20 @@ _lib.moe_ep_owner_forward.argtypes = [ctypes.POINTER(EpOwnerArgs), _I, _P, _S, _
 _lib.moe_ep_home_combine.argtypes = [_P, _P, _P, _P, _I, _I, _I, _P, _P, _I, _P]
 _lib.moe_ep_debug_plan.argtypes = [_P, _I, _I, _I, _I, _I, _P, _P, _I]
 _lib.moe_ep_debug_plan.restype = _I
+_lib.moe_route_scored.argtypes = [_P, _I, _I, _I, ctypes.POINTER(RouterArgs), _P, _P, _P, _P, _S, _P]
+_lib.moe_route_scored_backward.argtypes = [_P, _P, _P, _I, _I, _I, ctypes.POINTER(RouterArgs), _P, _P]
+_lib.moe_layer_forward_scored.argtypes = [ctypes.POINTER(LayerArgs), ctypes.POINTER(RouterArgs), _I, _P,
+                                          _S, _P]
+_lib.moe_combine_backward.argtypes = [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P]
+_lib.moe_linear_workspace_size.argtypes = [_I, _I, _I]
+_lib.moe_linear_workspace_size.restype = _S
+_lib.moe_linear_backward_workspace_size.argtypes = [_I, _I, _I]
+_lib.moe_linear_backward_workspace_size.restype = _S
+_lib.moe_linear.argtypes = [ctypes.POINTER(LinearArgs), _P, _S, _P]
+_lib.moe_linear_backward.argtypes = [ctypes.POINTER(LinearBwdArgs), _P, _S, _P]
+for _fn in ("moe_route_scored", "moe_route_scored_backward", "moe_layer_forward_scored",
+            "moe_combine_backward", "moe_linear", "moe_linear_backward"):
+    getattr(_lib, _fn).restype = _I
 for _fn in ("moe_route", "moe_permute", "moe_grouped_ffn", "moe_combine", "moe_layer_forward",
             "moe_get_status", "moe_ep_owner_forward", "moe_ep_home_combine"):
     getattr(_lib, _fn).restype = _I
@@ -310,8 +357,10 @@ def make_args(x, logits, W1, W3, W2, k, out, topk_idx=None, topk_gate=None, coun
 
 def layer_forward(x, logits, W1, W3, W2, k, ws, mode=MODE_OVERLAPPED, out=None, outputs=False,
                   consumer_sms=0, mgb=1, flags=0, timeout_us=0, stream=None, ev_begin=None,
-                  ev_end=None, d_ff=None):
+                  ev_end=None, d_ff=None, router=None):
     """One MoE layer.  Returns out, or (out, dict of routing outputs) if outputs.
+    router: a Router, for its routing (moe_layer_forward_scored) in the place of the
+    softmax over the chosen logits.
     With flags DBG_IDENTITY_EXPERTS the weights may be None (then d_ff gives the
     FFN width the workspace was sized for)."""
     _need(x, torch.bfloat16, "x")
@@ -347,8 +396,13 @@ def layer_forward(x, logits, W1, W3, W2, k, ws, mode=MODE_OVERLAPPED, out=None, 
                      flags=flags, timeout_us=timeout_us, ev_begin=ev_begin, ev_end=ev_end,
                      d_ff=f, **extra)
 
-    _check(_lib.moe_layer_forward(ctypes.byref(args), int(mode), _ptr(ws), ws.numel(),
-                                  _stream(stream)), "moe_layer_forward")
+    if router is not None:
+        _check(_lib.moe_layer_forward_scored(ctypes.byref(args), ctypes.byref(router.args(E, dev)), int(mode),
+                                             _ptr(ws), ws.numel(), _stream(stream)),
+               "moe_layer_forward_scored")
+    else:
+        _check(_lib.moe_layer_forward(ctypes.byref(args), int(mode), _ptr(ws), ws.numel(),
+                                      _stream(stream)), "moe_layer_forward")
     return (out, extra) if outputs else out
 
 
@@ -393,19 +447,281 @@ def debug_tokens_combined(ws: torch.Tensor, T: int, d: int, f: int, E: int, k: i
     return int(n.value)
 
 
-class MoELayer:
-    """Holds the weights and a workspace; forward() runs the layer."""
+# ---- the linear layer, the scored router and their gradients ----------------
+def _same_device(*named):
+    """Every given tensor on one device, the current one: the library launches there."""
+    cur = torch.cuda.current_device()
+    for t, name in named:
+        if t is not None and t.get_device() != cur:
+            raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{cur}")
 
-    def __init__(self, W1, W3, W2, k: int, max_tokens: int):
+
+def _dtype_code(dtype, name: str) -> int:
+    if dtype is torch.bfloat16:
+        return DTYPE_BF16
+    if dtype is torch.float32:
+        return DTYPE_F32
+    raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {dtype}")
+
+
+def _need2(t, dtype, name: str):
+    _need(t, dtype, name)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
+
+
+def _scratch(ws, need: int, device, what: str):
+    """The caller's workspace, or one from torch's allocator (of the current stream)."""
+    if need >= 1 << 62:
+        raise MoEError(MOE_ERR_INVALID, what)
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    _need(ws, torch.uint8, "ws")
+    if ws.numel() < need:
+        raise ValueError(f"workspace smaller than {what} for this shape")
+    return ws
+
+
+def linear_workspace_size(M: int, K: int, N: int) -> int:
+    return int(_lib.moe_linear_workspace_size(M, K, N))
+
+
+def linear_backward_workspace_size(M: int, K: int, N: int) -> int:
+    return int(_lib.moe_linear_backward_workspace_size(M, K, N))
+
+
+def linear(x, W, bias=None, residual=None, act=ACT_NONE, out_dtype=torch.bfloat16, pre=False, out=None,
+           ws=None, stream=None):
+    """out = act(x W + bias) + residual (moe_linear): x [M][K], W [K][N] bf16, bias [N]
+    fp32, residual and out [M][N] of out_dtype (bf16 or fp32; out may be residual).
+    pre=True also returns x W + bias in bf16, which linear_backward wants with an
+    activation.  ws: linear_workspace_size(M, K, N) bytes (None: allocated here)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear(x, W, bias, residual, act, out_dtype, pre, out, ws)
+    _need2(x, torch.bfloat16, "x")
+    _need2(W, torch.bfloat16, "W")
+    M, K = x.shape
+    N = W.shape[1]
+    _shape(W, (K, N), "W")
+    code = _dtype_code(out_dtype, "out_dtype")
+    if bias is not None:
+        _need(bias, torch.float32, "bias")
+        _shape(bias, (N,), "bias")
+    if residual is not None:
+        _need(residual, out_dtype, "residual")
+        _shape(residual, (M, N), "residual")
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+    else:
+        _need(out, out_dtype, "out")
+        _shape(out, (M, N), "out")
+    u = torch.empty((M, N), dtype=torch.bfloat16, device=x.device) if pre else None
+    ws = _scratch(ws, _lib.moe_linear_workspace_size(M, K, N), x.device, "moe_linear_workspace_size")
+    _same_device((x, "x"), (W, "W"), (bias, "bias"), (residual, "residual"), (out, "out"), (ws, "ws"))
+    a = LinearArgs(M, K, N, x.data_ptr(), W.data_ptr(), None if bias is None else bias.data_ptr(),
+                   None if residual is None else residual.data_ptr(), int(act), code, out.data_ptr(),
+                   None if u is None else u.data_ptr())
+    _check(_lib.moe_linear(ctypes.byref(a), _ptr(ws), 0 if ws is None else ws.numel(), _stream()), "moe_linear")
+    return (out, u) if pre else out
+
+
+def linear_backward(dout, x, W, pre=None, act=ACT_NONE, dW_dtype=torch.float32, want_dx=True, want_dW=True,
+                    want_dbias=False, ws=None, stream=None):
+    """The gradients of linear (moe_linear_backward): dout [M][N] bf16 or fp32 ->
+    (dx [M][K] bf16, dW [K][N] of dW_dtype, dbias [N] fp32), None where not wanted.
+    The residual's gradient is dout itself.  pre: linear's second result, with an
+    activation.  ws: linear_backward_workspace_size(M, K, N) bytes (None: allocated here)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear_backward(dout, x, W, pre, act, dW_dtype, want_dx, want_dW, want_dbias, ws)
+    _need2(x, torch.bfloat16, "x")
+    _need2(W, torch.bfloat16, "W")
+    M, K = x.shape
+    N = W.shape[1]
+    _shape(W, (K, N), "W")
+    code, dW_code = _dtype_code(dout.dtype, "dout"), _dtype_code(dW_dtype, "dW_dtype")
+    _need(dout, dout.dtype, "dout")
+    _shape(dout, (M, N), "dout")
+    if act != ACT_NONE:
+        if pre is None:
+            raise ValueError("linear_backward needs pre (linear(..., pre=True)) with an activation")
+        _need(pre, torch.bfloat16, "pre")
+        _shape(pre, (M, N), "pre")
+    else:
+        pre = None
+    dev = x.device
+    dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev) if want_dx else None
+    dW = torch.empty((K, N), dtype=dW_dtype, device=dev) if want_dW else None
+    db = torch.empty(N, dtype=torch.float32, device=dev) if want_dbias else None
+    ws = _scratch(ws, _lib.moe_linear_backward_workspace_size(M, K, N), dev,
+                  "moe_linear_backward_workspace_size")
+    _same_device((x, "x"), (W, "W"), (dout, "dout"), (pre, "pre"), (ws, "ws"))
+    p = [None if t is None else t.data_ptr() for t in (pre, dx, dW, db)]
+    a = LinearBwdArgs(M, K, N, dout.data_ptr(), x.data_ptr(), W.data_ptr(), p[0], int(act), code, dW_code,
+                      p[1], p[2], p[3])
+    _check(_lib.moe_linear_backward(ctypes.byref(a), _ptr(ws), 0 if ws is None else ws.numel(), _stream()),
+           "moe_linear_backward")
+    return dx, dW, db
+
+
+def _router_args(E, device, score, bias, n_groups, topk_groups, group_score, renorm, scale) -> RouterArgs:
+    if bias is not None:
+        _need(bias, torch.float32, "bias")
+        _shape(bias, (E,), "bias")
+        if bias.device != device:
+            raise ValueError(f"bias is on {bias.device}, the logits on {device}")
+    return RouterArgs(int(score), None if bias is None else bias.data_ptr(), int(n_groups), int(topk_groups),
+                      int(group_score), 1 if renorm else 0, float(scale))
+
+
+def route_scored(logits, k: int, score=SCORE_SOFTMAX, bias=None, n_groups=1, topk_groups=0,
+                 group_score=GROUP_MAX, renorm=True, scale=1.0, counts=False, ws=None, stream=None):
+    """The scored router (moe_route_scored): logits [T][E] fp32 -> (topk_idx [T][k] int32,
+    topk_gate [T][k] fp32), and counts [E] int32 with counts=True (then ws, of
+    alloc_workspace, is needed).  bias [E] fp32 steers the choice only."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return route_scored(logits, k, score, bias, n_groups, topk_groups, group_score, renorm, scale,
+                                counts, ws)
+    _need2(logits, torch.float32, "logits")
+    T, E = logits.shape
+    dev = logits.device
+    r = _router_args(E, dev, score, bias, n_groups, topk_groups, group_score, renorm, scale)
+    idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+    gate = torch.empty((T, k), dtype=torch.float32, device=dev)
+    cnt = torch.empty(E, dtype=torch.int32, device=dev) if counts else None
+    _same_device((logits, "logits"), (ws, "ws"))
+    _check(_lib.moe_route_scored(_ptr(logits), T, E, k, ctypes.byref(r), _ptr(idx), _ptr(gate), _ptr(cnt),
+                                 _ptr(ws), 0 if ws is None else ws.numel(), _stream()), "moe_route_scored")
+    return (idx, gate, cnt) if counts else (idx, gate)
+
+
+def route_scored_backward(dgate, logits, topk_idx, score=SCORE_SOFTMAX, renorm=True, scale=1.0,
+                          dlogits=None, stream=None):
+    """The gradient of route_scored's gates (moe_route_scored_backward): dgate [T][k]
+    -> dlogits [T][E], all of it written."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return route_scored_backward(dgate, logits, topk_idx, score, renorm, scale, dlogits)
+    _need2(logits, torch.float32, "logits")
+    _need2(dgate, torch.float32, "dgate")
+    _need(topk_idx, torch.int32, "topk_idx")
+    T, E = logits.shape
+    k = dgate.shape[1]
+    _shape(dgate, (T, k), "dgate")
+    _shape(topk_idx, (T, k), "topk_idx")
+    if dlogits is None:
+        dlogits = torch.empty((T, E), dtype=torch.float32, device=logits.device)
+    else:
+        _need(dlogits, torch.float32, "dlogits")
+        _shape(dlogits, (T, E), "dlogits")
+    _same_device((logits, "logits"), (dgate, "dgate"), (topk_idx, "topk_idx"), (dlogits, "dlogits"))
+    r = _router_args(E, logits.device, score, None, 1, 0, GROUP_MAX, renorm, scale)
+    _check(_lib.moe_route_scored_backward(_ptr(dgate), _ptr(logits), _ptr(topk_idx), T, E, k, ctypes.byref(r),
+                                          _ptr(dlogits), _stream()), "moe_route_scored_backward")
+    return dlogits
+
+
+def combine_backward(dout, y, row_of, topk_gate, want_dy=True, dy=None, stream=None):
+    """The gradient of combine (moe_combine_backward): dout [T][d] bf16 -> (dy [T*k][d]
+    bf16 or None, dgate [T][k] fp32).  A row_of of -1 is a dropped slot (dgate 0); rows of
+    dy that no slot names are left as they were (uninitialised, if dy is allocated here)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return combine_backward(dout, y, row_of, topk_gate, want_dy, dy)
+    _need2(dout, torch.bfloat16, "dout")
+    _need2(y, torch.bfloat16, "y")
+    _need(row_of, torch.int32, "row_of")
+    _need2(topk_gate, torch.float32, "topk_gate")
+    T, k = topk_gate.shape
+    d = y.shape[1]
+    _shape(dout, (T, d), "dout")
+    _shape(y, (T * k, d), "y")
+    _shape(row_of, (T * k,), "row_of")
+    if dy is not None:
+        _need(dy, torch.bfloat16, "dy")
+        _shape(dy, (T * k, d), "dy")
+    elif want_dy:
+        dy = torch.empty((T * k, d), dtype=torch.bfloat16, device=y.device)
+    dgate = torch.empty((T, k), dtype=torch.float32, device=y.device)
+    _same_device((dout, "dout"), (y, "y"), (row_of, "row_of"), (topk_gate, "topk_gate"), (dy, "dy"))
+    _check(_lib.moe_combine_backward(_ptr(dout), _ptr(y), _ptr(row_of), _ptr(topk_gate), T, d, k, _ptr(dy),
+                                     _ptr(dgate), _stream()), "moe_combine_backward")
+    return dy, dgate
+
+
+class Router:
+    """A router's options, and with Wg [d][E] bf16 (and bg [E] fp32) its gate projection."""
+
+    def __init__(self, Wg=None, bg=None, score=SCORE_SOFTMAX, bias=None, n_groups=1, topk_groups=0,
+                 group_score=GROUP_MAX, renorm=True, scale=1.0):
+        self.Wg, self.bg, self.score, self.bias = Wg, bg, score, bias
+        self.n_groups, self.topk_groups, self.group_score = n_groups, topk_groups, group_score
+        self.renorm, self.scale = renorm, scale
+
+    def args(self, E: int, device) -> RouterArgs:
+        return _router_args(E, device, self.score, self.bias, self.n_groups, self.topk_groups,
+                            self.group_score, self.renorm, self.scale)
+
+    def logits(self, x, stream=None):
+        """The gate projection x Wg + bg in fp32."""
+        if self.Wg is None:
+            raise ValueError("this Router has no gate projection (Wg)")
+        return linear(x, self.Wg, bias=self.bg, out_dtype=torch.float32, stream=stream)
+
+    def route(self, logits, k: int, **kw):
+        return route_scored(logits, k, self.score, self.bias, self.n_groups, self.topk_groups,
+                            self.group_score, self.renorm, self.scale, **kw)
+
+    def backward(self, dgate, logits, topk_idx, stream=None):
+        return route_scored_backward(dgate, logits, topk_idx, self.score, self.renorm, self.scale,
+                                     stream=stream)
+
+
+class MoELayer:
+    """Holds the weights and a workspace; forward() runs the layer.  With a Router that
+    has a gate projection, forward(x) makes the logits too, and forward_train / backward
+    train the router over the (frozen) experts."""
+
+    def __init__(self, W1, W3, W2, k: int, max_tokens: int, router: Router | None = None):
         self.W1, self.W3, self.W2, self.k = W1, W3, W2, k
         self.E, self.d, self.f = W1.shape
         self.max_tokens = max_tokens
+        self.router = router
         self.ws = alloc_workspace(max_tokens, self.d, self.f, self.E, k, W1.device)
 
-    def forward(self, x, logits, mode=MODE_OVERLAPPED, **kw):
+    def forward(self, x, logits=None, mode=MODE_OVERLAPPED, **kw):
         if x.shape[0] > self.max_tokens:
             raise ValueError("more tokens than the workspace was sized for")
-        return layer_forward(x, logits, self.W1, self.W3, self.W2, self.k, self.ws, mode, **kw)
+        if logits is None:
+            if self.router is None:
+                raise ValueError("logits are needed without a Router")
+            logits = self.router.logits(x, stream=kw.get("stream"))
+        return layer_forward(x, logits, self.W1, self.W3, self.W2, self.k, self.ws, mode,
+                             router=self.router, **kw)
+
+    def forward_train(self, x):
+        """The layer step by step: (out, saved), with what backward needs."""
+        if x.shape[0] > self.max_tokens:
+            raise ValueError("more tokens than the workspace was sized for")
+        if self.router is None:
+            raise ValueError("forward_train needs a Router")
+        logits = self.router.logits(x)
+        idx, gate = self.router.route(logits, self.k)
+        _, offsets, _, row_of, x_perm = permute(x, idx, self.E, self.ws)
+        _, y = grouped_ffn(x_perm, offsets, self.W1, self.W3, self.W2, x.shape[0], self.k, self.ws, want_h=False)
+        return combine(y, row_of, gate), dict(x=x, logits=logits, idx=idx, gate=gate, row_of=row_of, y=y)
+
+    def backward(self, dout, saved, want_dy=False):
+        """Gradients of the router from dout [T][d] bf16 and forward_train's saved: a dict
+        of dWg, dbg (fp32; dbg None without bg), dx (the gate projection's share, bf16),
+        dlogits, and with want_dy dy [T*k][d], the gradient of the experts' outputs."""
+        r = self.router
+        dy, dgate = combine_backward(dout, saved["y"], saved["row_of"], saved["gate"], want_dy=want_dy)
+        dlogits = r.backward(dgate, saved["logits"], saved["idx"])
+        dx, dWg, dbg = linear_backward(dlogits, saved["x"], r.Wg, want_dbias=r.bg is not None)
+        return dict(dWg=dWg, dbg=dbg, dx=dx, dlogits=dlogits, dy=dy)
 
 
 # ---- expert parallelism: the fused return -----------------------------------

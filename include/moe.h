@@ -250,6 +250,121 @@ size_t moe_permute_noalloc_scratch_bytes(void);
 moe_status moe_layer_forward(const moe_layer_args* args, moe_mode mode,
                              void* ws, size_t ws_bytes, void* stream);
 
+/* ---- The scored router -----------------------------------------------------
+ * Routing in the forms that trained MoE layers use.  With z = logits[t]:
+ *   score  p_e = exp(z_e) / sum_i exp(z_i) over all E   (MOE_SCORE_SOFTMAX)
+ *          p_e = 1 / (1 + exp(-z_e))                    (MOE_SCORE_SIGMOID)
+ *   key    z_e without a bias (the order of the scores without their rounding),
+ *          p_e + bias_e with one; the bias steers the choice only, no gate sees it
+ *   groups the experts in n_groups runs of E / n_groups; a group's value is its
+ *          largest key (MOE_GROUP_MAX) or the sum of its two largest p_e (+ bias_e)
+ *          (MOE_GROUP_TOP2); only the topk_groups best groups' experts are chosen from
+ *   chosen the k largest keys, by key descending; keys and group values are compared
+ *          as 64-bit values, ties go to the lower expert (group) id
+ *   gate   scale * p_e, or scale * p_e / (sum of the k chosen p) with renorm
+ *          (0 where that sum is 0).
+ * A logit of -infinity or NaN masks its expert: its score is 0, it comes after every
+ * other expert of the chosen groups (by id), a group counts its other experts only
+ * and a group of masked experts comes last; a token with fewer than k experts left
+ * gets masked ones with a gate of 0.  A logit of +infinity counts as FLT_MAX. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score;
+
+typedef struct {
+  int score;                /* moe_score                                             */
+  const float* bias;        /* [E] finite selection bias, or NULL                    */
+  int n_groups;             /* 1..32, dividing E; 0 = 1 (no groups)                  */
+  int topk_groups;          /* 1..n_groups, with k <= topk_groups * E / n_groups; 0 = n_groups */
+  int group_score;          /* moe_group_score (read with topk_groups < n_groups)    */
+  int renorm;               /* 0: gate = scale * p;  1: divided by the chosen p's sum */
+  float scale;              /* finite                                                */
+} moe_router;
+
+/* logits [T][E] fp32 -> topk_idx [T][k] int32, topk_gate [T][k] fp32; counts [E]
+ * int32 (optional): routed rows per expert.  ws is needed (moe_workspace_size, any d
+ * and f) with counts only, and may be NULL otherwise.  router is a HOST pointer, read
+ * before the call returns; router->bias is a device pointer. */
+moe_status moe_route_scored(const float* logits, int T, int E, int k, const moe_router* router,
+                            int32_t* topk_idx, float* topk_gate, int32_t* counts, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* The gradient of moe_route_scored's gates: dgate [T][k] fp32 and the forward's
+ * logits and topk_idx -> dlogits [T][E] fp32 (every element is written).  The choice
+ * itself has no gradient, nor has the bias; masked experts get 0, and so does a row
+ * whose renormalising sum is 0.  A topk_idx outside [0, E) is skipped (a dropped
+ * slot); an id may stand in a row once only.  Of the router, score, renorm and scale
+ * are read. */
+moe_status moe_route_scored_backward(const float* dgate, const float* logits,
+                                     const int32_t* topk_idx, int T, int E, int k,
+                                     const moe_router* router, float* dlogits, void* stream);
+
+/* moe_layer_forward with the scored router in the place of step (a). */
+moe_status moe_layer_forward_scored(const moe_layer_args* args, const moe_router* router,
+                                    moe_mode mode, void* ws, size_t ws_bytes, void* stream);
+
+/* The gradient of moe_combine: with r = row_of[t*k + j],
+ *   dy[r] = bf16(topk_gate[t][j] * dout[t]),   dgate[t][j] = sum_c dout[t][c] * y[r][c]
+ * (fp32 sums in a fixed order).  dout [T][d] bf16, y [T*k][d] bf16, row_of [T*k],
+ * topk_gate [T][k] -> dy [T*k][d] bf16 (optional, NULL: frozen experts need none),
+ * dgate [T][k] fp32.  A row_of outside [0, T*k) is a dropped slot: its dgate is 0 and
+ * it has no row; rows of dy that no slot names are left as they were. */
+moe_status moe_combine_backward(const void* dout, const void* y, const int32_t* row_of,
+                                const float* topk_gate, int T, int d, int k, void* dy,
+                                float* dgate, void* stream);
+
+/* ---- The linear layer -------------------------------------------------------
+ * The dense products around the experts: the gate projection that makes the logits,
+ * and a shared expert's up and down projections.
+ *   u = x W + bias,   out = act(u) + residual
+ * accumulated in fp32 and rounded once.  Any M, K, N >= 1 (rows that are not 16-byte
+ * multiples are first copied into padded ones in the workspace); sums run in an
+ * order that depends on the shape alone, so equal calls give equal bits. */
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 /* erf */ } moe_act;
+typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 } moe_dtype;
+
+typedef struct {
+  int M, K, N;
+  const void* x;            /* [M][K] bf16                                           */
+  const void* W;            /* [K][N] bf16                                           */
+  const float* bias;        /* [N] fp32, or NULL                                     */
+  const void* residual;     /* [M][N] of out_dtype, or NULL; may be out itself       */
+  int act;                  /* moe_act                                               */
+  int out_dtype;            /* moe_dtype                                             */
+  void* out;                /* [M][N] of out_dtype                                   */
+  void* pre;                /* [M][N] bf16: u, for the backward pass; or NULL        */
+} moe_linear_args;
+
+/* Workspace bytes (0: none needed, ws may be NULL; SIZE_MAX on an invalid shape). */
+size_t moe_linear_workspace_size(int M, int K, int N);
+
+moe_status moe_linear(const moe_linear_args* args, void* ws, size_t ws_bytes, void* stream);
+
+/* The gradients:  du = dout * act'(pre),
+ *   dx = du W^T,   dW = x^T du,   dbias = sum_m du      (d residual is dout itself).
+ * Each output is optional.  pre is read with an activation only.  dout is bf16 or
+ * fp32.  The products run on bf16 operands: an fp32 du goes in as a sum of bf16 terms
+ * -- three (all 24 bits) for a dW in fp32, two for bf16 gradients, or one where the
+ * product is large enough to be bound by the tensor cores (then du is rounded to
+ * bf16 once, as a stored activation gradient would be). */
+typedef struct {
+  int M, K, N;
+  const void* dout;         /* [M][N] of dout_dtype                                  */
+  const void* x;            /* [M][K] bf16 (dW)                                      */
+  const void* W;            /* [K][N] bf16 (dx)                                      */
+  const void* pre;          /* [M][N] bf16, with an activation                       */
+  int act;                  /* moe_act                                               */
+  int dout_dtype;           /* moe_dtype                                             */
+  int dW_dtype;             /* moe_dtype                                             */
+  void* dx;                 /* [M][K] bf16, or NULL                                  */
+  void* dW;                 /* [K][N] of dW_dtype, or NULL                           */
+  float* dbias;             /* [N] fp32, or NULL                                     */
+} moe_linear_bwd_args;
+
+size_t moe_linear_backward_workspace_size(int M, int K, int N);
+
+moe_status moe_linear_backward(const moe_linear_bwd_args* args, void* ws, size_t ws_bytes,
+                               void* stream);
+
 /* ---- Expert parallelism: the fused return ---------------------------------
  * W ranks; rank o owns the local experts [o*El, (o+1)*El) of E = W*El.  Each
  * home rank routes and permutes its own tokens (moe_route, moe_permute); its
