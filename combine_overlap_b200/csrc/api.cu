@@ -588,6 +588,12 @@ moe_status moe_linear_backward(const moe_linear_bwd_args* args, void* ws, size_t
   return cuda_status(launch_linear_bwd(a, ws, static_cast<cudaStream_t>(stream)));
 }
 
+moe_status moe_linear_get_status(void* stream) {
+  uint32_t word = 0;
+  MOE_TRY(linear_timeout(static_cast<cudaStream_t>(stream), &word));
+  return word ? MOE_ERR_TIMEOUT : MOE_OK;
+}
+
 size_t moe_ep_owner_workspace_size(int N, int d, int f, int El, int W) {
   if (N < 0 || d < 1 || f < 1 || El < 1 || W < 1 || W > MAX_W || (long long)El * W > MAX_E) return 0;
   if (d % BN2 != 0 || f % BN1 != 0) return 0;

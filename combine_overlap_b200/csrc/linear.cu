@@ -1,20 +1,17 @@
-// linear.cu -- the linear layer (moe_linear) and its gradients: products with bias,
-// activation and residual in the epilogue (include/moe.h states the formulas).
-#include "kernels.h"
+// linear.cu -- the linear layer (moe_linear) and its gradients (include/moe.h states the
+// formulas): what stands before and beside the tensor-core products of gemm.cu.
+//
+//   pack      rows that are no multiple of 16 bytes (TMA's stride rule) -> padded copies
+//   dact      du = dout act'(pre) as bf16 terms, and per block of rows du's column sums
+//   dbias     the sums of those sums
+#include "gemm.cuh"
 #include "combine.cuh"
 
 #include <math.h>
 
 namespace moe {
 
-__device__ __forceinline__ float act_f32(int act, float u) {
-  switch (act) {
-    case 1: return fmaxf(u, 0.0f);
-    case 2: return u / (1.0f + expf(-u));
-    case 3: return 0.5f * u * (1.0f + erff(u * 0.70710678f));
-  }
-  return u;
-}
+namespace {
 
 __device__ __forceinline__ float dact_f32(int act, float u) {
   switch (act) {
@@ -28,145 +25,227 @@ __device__ __forceinline__ float dact_f32(int act, float u) {
   return 1.0f;
 }
 
-// An operand of a product: element (i, j) at p[i * si + j * sj], bf16 or fp32.
-struct Operand {
-  const void* p;
-  long si, sj;
-  int f32;
-};
+inline int pad8(int n) { return cdiv(n, 8) * 8; }
+inline size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-__device__ __forceinline__ float load_op(const Operand& o, long i, long j) {
-  const long at = i * o.si + j * o.sj;
-  return o.f32 ? static_cast<const float*>(o.p)[at]
-               : __bfloat162float(static_cast<const __nv_bfloat16*>(o.p)[at]);
-}
-
-// C[m][n] = epilogue( sum_k A(m, k) B(k, n) ): 64 x 64 tiles, 16-deep steps, 4 x 4
-// sums per thread in fp32.  For any sizes, strides and types.
-__global__ void __launch_bounds__(256) gemm_simple_kernel(Operand A, Operand B, int M, int N, int K,
-                                                          const LinearEpi ep) {
+// ------------------------------------------------------------------- pack ---
+// [rows][n] -> [rows][n8], the pad zero: one thread per 8 output columns.
+__global__ void __launch_bounds__(256) pack_kernel(const __nv_bfloat16* __restrict__ in, long rows, int n,
+                                                   int n8, uint4* __restrict__ out) {
   pdl_trigger();
   pdl_wait();
-  __shared__ float sa[16][65], sb[16][65];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int m0 = blockIdx.x * 64, n0 = blockIdx.y * 64;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < K; k0 += 16) {
-    for (int i = threadIdx.x; i < 1024; i += 256) {
-      const int kk = A.sj == 1 ? i & 15 : i >> 6, mm = A.sj == 1 ? i >> 4 : i & 63;
-      sa[kk][mm] = (m0 + mm < M && k0 + kk < K) ? load_op(A, m0 + mm, k0 + kk) : 0.0f;
-      const int kb = B.sj == 1 ? i >> 6 : i & 15, nn = B.sj == 1 ? i & 63 : i >> 4;
-      sb[kb][nn] = (n0 + nn < N && k0 + kb < K) ? load_op(B, k0 + kb, n0 + nn) : 0.0f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < 16; ++kk) {
-      float a[4], b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) { a[i] = sa[kk][ty * 4 + i]; b[i] = sb[kk][tx * 4 + i]; }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  const long per = n8 / 8, total = rows * per;
+  for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long)gridDim.x * 256) {
+    const long r = i / per;
+    const int c = (int)(i - r * per) * 8;
+    const unsigned short* src = reinterpret_cast<const unsigned short*>(in) + r * n + c;
+    uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-      if (m >= M || n >= N) continue;
-      const size_t at = (size_t)m * N + n;
-      float u = acc[i][j] + (ep.bias ? ep.bias[n] : 0.0f);
-      if (ep.pre) static_cast<__nv_bfloat16*>(ep.pre)[at] = __float2bfloat16(u);
-      float v = act_f32(ep.act, u);
-      if (ep.residual)
-        v += ep.out_f32 ? static_cast<const float*>(ep.residual)[at]
-                        : __bfloat162float(static_cast<const __nv_bfloat16*>(ep.residual)[at]);
-      if (ep.out_f32) static_cast<float*>(ep.out)[at] = v;
-      else static_cast<__nv_bfloat16*>(ep.out)[at] = __float2bfloat16(v);
+      const uint32_t lo = c + 2 * j < n ? src[2 * j] : 0u, hi = c + 2 * j + 1 < n ? src[2 * j + 1] : 0u;
+      w[j] = lo | hi << 16;
     }
+    out[i] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
-static cudaError_t gemm_simple(const Operand& A, const Operand& B, int M, int N, int K, const LinearEpi& ep,
-                               cudaStream_t s) {
-  return launch_pdl(gemm_simple_kernel, dim3(cdiv(M, 64), cdiv(N, 64)), dim3(256), 0, s, A, B, M, N, K, ep);
+// `in` as an operand: itself, or its padded copy at `at` (advanced past it).
+cudaError_t pack(const void* in, long rows, int n, char** at, GemmOperand* o, cudaStream_t s) {
+  const int n8 = pad8(n);
+  o->ld = (size_t)n8 * 2;
+  o->plane = 0;
+  o->planes = 1;
+  o->p = in;
+  if (n8 == n) return cudaSuccess;
+  o->p = *at;
+  uint4* out = reinterpret_cast<uint4*>(*at);
+  *at += up256((size_t)rows * n8 * 2);
+  const long total = rows * (n8 / 8);
+  const int grid = (int)(total + 255 < 148L * 16 * 256 ? (total + 255) / 256 : 148L * 16);
+  return launch_pdl(pack_kernel, dim3(grid), dim3(256), 0, s, static_cast<const __nv_bfloat16*>(in), rows, n,
+                    n8, out);
 }
 
-// du = dout * act'(pre), and per block of rows the column sums of du.
+size_t pack_bytes(long rows, int n) { return n % 8 ? up256((size_t)rows * pad8(n) * 2) : 0; }
+
+// ------------------------------------------------------------------- dact ---
+// A block takes 128 columns (16 threads of 8) and `rows` rows, 16 at a time.  du's
+// planes: plane 0 = bf16(du), plane p = bf16(du - the earlier planes).  `part`
+// [gridDim.y][N] (optional): the block's column sums, in a fixed order.
 __global__ void __launch_bounds__(256) dact_kernel(const void* __restrict__ dout, int f32,
                                                    const __nv_bfloat16* __restrict__ pre, int act, int M,
-                                                   int N, int rows, float* __restrict__ du,
-                                                   float* __restrict__ part) {
+                                                   int N, int rows, int planes, __nv_bfloat16* __restrict__ du,
+                                                   size_t plane, int n8, float* __restrict__ part) {
   pdl_trigger();
   pdl_wait();
-  const int n = blockIdx.x * 256 + threadIdx.x;
-  if (n >= N) return;
-  float sum = 0.0f;
-  for (int m = blockIdx.y * rows; m < min(M, (int)(blockIdx.y + 1) * rows); ++m) {
-    const size_t at = (size_t)m * N + n;
-    float v = f32 ? static_cast<const float*>(dout)[at]
-                  : __bfloat162float(static_cast<const __nv_bfloat16*>(dout)[at]);
-    if (act) v *= dact_f32(act, __bfloat162float(pre[at]));
-    du[at] = v;
-    sum += v;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int n = blockIdx.x * 128 + tx * 8;
+  const bool vec = (N & 7) == 0;
+  const int m1 = min(M, (int)(blockIdx.y + 1) * rows);
+  float sum[8] = {};
+  if (n < n8) {
+    for (int m = blockIdx.y * rows + ty; m < m1; m += 16) {
+      const size_t at = (size_t)m * N + n;
+      float v[8] = {}, u[8] = {};
+      if (vec) {
+        if (f32) {
+          const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(dout) + at));
+          const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(dout) + at) + 1);
+          v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+          bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(dout) + at)), v);
+        }
+        if (act) bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(pre + at)), u);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (n + i < N) {
+            v[i] = f32 ? static_cast<const float*>(dout)[at + i]
+                       : __bfloat162float(static_cast<const __nv_bfloat16*>(dout)[at + i]);
+            if (act) u[i] = __bfloat162float(pre[at + i]);
+          }
+        }
+      }
+      if (act) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= dact_f32(act, u[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += v[i];
+      for (int p = 0; p < planes; ++p) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+        *reinterpret_cast<uint4*>(du + p * plane + (size_t)m * n8 + n) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xffff0000u);
+          v[2 * i] = isfinite(lo) ? v[2 * i] - lo : 0.0f;   // an infinity has no remainder
+          v[2 * i + 1] = isfinite(hi) ? v[2 * i + 1] - hi : 0.0f;
+        }
+      }
+    }
   }
-  part[(size_t)blockIdx.y * N + n] = sum;
+  if (part == nullptr) return;
+  __shared__ float sh[16][129];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sh[ty][tx * 8 + i] = sum[i];
+  __syncthreads();
+  const int c = threadIdx.x;
+  if (c < 128 && blockIdx.x * 128 + c < N) {
+    float s = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s += sh[r][c];
+    part[(size_t)blockIdx.y * N + blockIdx.x * 128 + c] = s;
+  }
 }
 
+// 32 columns per block, 8 warps each a run of the blocks' sums.
 __global__ void __launch_bounds__(256) dbias_kernel(const float* __restrict__ part, int nblk, int N,
                                                     float* __restrict__ dbias) {
   pdl_trigger();
   pdl_wait();
-  const int n = blockIdx.x * 256 + threadIdx.x;
-  if (n >= N) return;
+  __shared__ float sh[8][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int n = blockIdx.x * 32 + lane;
   float sum = 0.0f;
-  for (int b = 0; b < nblk; ++b) sum += part[(size_t)b * N + n];
-  dbias[n] = sum;
+  if (n < N)
+    for (int b = w; b < nblk; b += 8) sum += part[(size_t)b * N + n];
+  sh[w][lane] = sum;
+  __syncthreads();
+  if (w == 0 && n < N) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += sh[i][lane];
+    dbias[n] = s;
+  }
 }
 
-constexpr int DACT_ROWS = 128;
+// Rows per dact block: 16 at the least, so that a block has work, and not so few that
+// there are more than 256 blocks of rows.
+int dact_rows(int M) { return max(16, cdiv(cdiv(M, 256), 16) * 16); }
 
-size_t linear_ws_bytes(int M, int K, int N) {
-  (void)M; (void)K; (void)N;
-  return 0;
+// The bf16 terms that du goes in as.  dout in bf16 without an activation is du itself.
+struct Terms { int dx, dW, n; };
+Terms terms_of(const LinearBwdArgs& a) {
+  Terms t;
+  const bool exact = !a.dout_f32 && !a.act;
+  // bf16 gradients: one rounding of du where every side of the products is long
+  const int low = exact || (a.M > 256 && a.K > 256 && a.N > 256) ? 1 : 2;
+  t.dx = a.dx ? low : 0;
+  t.dW = a.dW ? (exact ? 1 : a.dW_f32 ? 3 : low) : 0;
+  t.n = max(t.dx, t.dW);
+  return t;
 }
+
+}  // namespace
+
+size_t linear_ws_bytes(int M, int K, int N) { return pack_bytes(M, K) + pack_bytes(K, N); }
 
 size_t linear_bwd_ws_bytes(int M, int K, int N) {
-  (void)K;
-  return (size_t)M * N * 4 + (size_t)cdiv(M, DACT_ROWS) * N * 4 + 256;
+  return up256((size_t)cdiv(M, dact_rows(M)) * N * 4) + 3 * up256((size_t)M * pad8(N) * 2) + pack_bytes(M, K) +
+         pack_bytes(K, N);
 }
 
 cudaError_t launch_linear(const LinearArgs& a, void* ws, cudaStream_t s) {
-  (void)ws;
-  return gemm_simple({a.x, a.K, 1, 0}, {a.W, a.N, 1, 0}, a.M, a.N, a.K, a.ep, s);
+  char* at = static_cast<char*>(ws);
+  GemmProblem p = {};
+  cudaError_t e = pack(a.x, a.M, a.K, &at, &p.A, s);
+  if (e == cudaSuccess) e = pack(a.W, a.K, a.N, &at, &p.B, s);
+  if (e != cudaSuccess) return e;
+  p.b_mn = 1;
+  p.M = a.M; p.N = a.N; p.K = a.K;
+  p.ep = a.ep;
+  return launch_gemm(p, s);
 }
 
 cudaError_t launch_linear_bwd(const LinearBwdArgs& a, void* ws, cudaStream_t s) {
-  float* du = static_cast<float*>(ws);
-  float* part = du + (size_t)a.M * a.N;
-  const int nblk = cdiv(a.M, DACT_ROWS);
-  cudaError_t e = launch_pdl(dact_kernel, dim3(cdiv(a.N, 256), nblk), dim3(256), 0, s, a.dout, a.dout_f32,
-                             static_cast<const __nv_bfloat16*>(a.pre), a.act, a.M, a.N, DACT_ROWS, du, part);
-  if (e != cudaSuccess) return e;
-  if (a.dbias) {
-    e = launch_pdl(dbias_kernel, dim3(cdiv(a.N, 256)), dim3(256), 0, s, (const float*)part, nblk, a.N, a.dbias);
+  char* at = static_cast<char*>(ws);
+  const int rows = dact_rows(a.M), nblk = cdiv(a.M, rows), n8 = pad8(a.N);
+  float* part = reinterpret_cast<float*>(at);
+  at += up256((size_t)nblk * a.N * 4);
+  const Terms t = terms_of(a);
+  GemmOperand du = {at, (size_t)n8 * 2, up256((size_t)a.M * n8 * 2), t.n};
+  at += 3 * du.plane;
+  // dout is an operand as it stands if it is bf16, unpadded and without an activation
+  const bool direct = !a.dout_f32 && !a.act && n8 == a.N;
+  if (!direct || a.dbias) {
+    cudaError_t e = launch_pdl(dact_kernel, dim3(cdiv(n8, 128), nblk), dim3(256), 0, s, a.dout, a.dout_f32,
+                               static_cast<const __nv_bfloat16*>(a.pre), a.act, a.M, a.N, rows,
+                               direct ? 0 : t.n, (__nv_bfloat16*)du.p, du.plane / 2, n8,
+                               a.dbias ? part : nullptr);
     if (e != cudaSuccess) return e;
   }
-  LinearEpi ep = {};
+  if (direct) du = {a.dout, (size_t)n8 * 2, 0, 1};
+  if (a.dbias) {
+    cudaError_t e = launch_pdl(dbias_kernel, dim3(cdiv(a.N, 32)), dim3(256), 0, s, (const float*)part, nblk,
+                               a.N, a.dbias);
+    if (e != cudaSuccess) return e;
+  }
   if (a.dx) {
-    ep.out = a.dx;
-    e = gemm_simple({du, a.N, 1, 1}, {a.W, 1, a.N, 0}, a.M, a.K, a.N, ep, s);
+    GemmProblem p = {};
+    cudaError_t e = pack(a.W, a.K, a.N, &at, &p.B, s);
+    if (e != cudaSuccess) return e;
+    p.A = du;
+    p.A.planes = t.dx;
+    p.M = a.M; p.N = a.K; p.K = a.N;
+    p.ep.out = a.dx;
+    e = launch_gemm(p, s);
     if (e != cudaSuccess) return e;
   }
   if (a.dW) {
-    ep.out = a.dW;
-    ep.out_f32 = a.dW_f32;
-    e = gemm_simple({a.x, 1, a.K, 0}, {du, a.N, 1, 1}, a.K, a.N, a.M, ep, s);
+    GemmProblem p = {};
+    cudaError_t e = pack(a.x, a.M, a.K, &at, &p.A, s);
+    if (e != cudaSuccess) return e;
+    p.B = du;
+    p.B.planes = t.dW;
+    p.a_mn = p.b_mn = 1;
+    p.M = a.K; p.N = a.N; p.K = a.M;
+    p.ep.out = a.dW;
+    p.ep.out_f32 = a.dW_f32;
+    return launch_gemm(p, s);
   }
-  return e;
+  return cudaSuccess;
 }
 
 }  // namespace moe

@@ -160,6 +160,8 @@ _lib.moe_linear_backward_workspace_size.argtypes = [_I, _I, _I]
 _lib.moe_linear_backward_workspace_size.restype = _S
 _lib.moe_linear.argtypes = [ctypes.POINTER(LinearArgs), _P, _S, _P]
 _lib.moe_linear_backward.argtypes = [ctypes.POINTER(LinearBwdArgs), _P, _S, _P]
+_lib.moe_linear_get_status.argtypes = [_P]
+_lib.moe_linear_get_status.restype = _I
 for _fn in ("moe_route_scored", "moe_route_scored_backward", "moe_layer_forward_scored",
             "moe_combine_backward", "moe_linear", "moe_linear_backward"):
     getattr(_lib, _fn).restype = _I
@@ -563,6 +565,12 @@ def linear_backward(dout, x, W, pre=None, act=ACT_NONE, dW_dtype=torch.float32, 
     _check(_lib.moe_linear_backward(ctypes.byref(a), _ptr(ws), 0 if ws is None else ws.numel(), _stream()),
            "moe_linear_backward")
     return dx, dW, db
+
+
+def linear_get_status(stream=None) -> int:
+    """Whether a bounded wait of linear or linear_backward ran out on the current device
+    since the last call of this (MOE_OK or MOE_ERR_TIMEOUT); syncs."""
+    return int(_lib.moe_linear_get_status(_stream(stream)))
 
 
 def _router_args(E, device, score, bias, n_groups, topk_groups, group_score, renorm, scale) -> RouterArgs:

@@ -365,6 +365,11 @@ size_t moe_linear_backward_workspace_size(int M, int K, int N);
 moe_status moe_linear_backward(const moe_linear_bwd_args* args, void* ws, size_t ws_bytes,
                                void* stream);
 
+/* Synchronises `stream`, then tells whether a bounded wait (2 s) of any moe_linear or
+ * moe_linear_backward on the current device ran out since the last call of this
+ * (MOE_ERR_TIMEOUT: those outputs are not to be used), and clears the note. */
+moe_status moe_linear_get_status(void* stream);
+
 /* ---- Expert parallelism: the fused return ---------------------------------
  * W ranks; rank o owns the local experts [o*El, (o+1)*El) of E = W*El.  Each
  * home rank routes and permutes its own tokens (moe_route, moe_permute); its
