@@ -165,15 +165,15 @@ __global__ void __launch_bounds__(256) dbias_kernel(const float* __restrict__ pa
 // there are more than 256 blocks of rows.
 int dact_rows(int M) { return max(16, cdiv(cdiv(M, 256), 16) * 16); }
 
-// The bf16 terms that du goes in as.  dout in bf16 without an activation is du itself.
+// The bf16 terms that du goes in as.  bf16 gradients take it rounded once, as a stored
+// bf16 gradient would be: an error of the size of their own rounding.  An fp32 dW takes
+// three terms, all 24 bits.  dout in bf16 without an activation is du itself.
 struct Terms { int dx, dW, n; };
 Terms terms_of(const LinearBwdArgs& a) {
   Terms t;
   const bool exact = !a.dout_f32 && !a.act;
-  // bf16 gradients: one rounding of du where every side of the products is long
-  const int low = exact || (a.M > 256 && a.K > 256 && a.N > 256) ? 1 : 2;
-  t.dx = a.dx ? low : 0;
-  t.dW = a.dW ? (exact ? 1 : a.dW_f32 ? 3 : low) : 0;
+  t.dx = a.dx ? 1 : 0;
+  t.dW = a.dW ? (!exact && a.dW_f32 ? 3 : 1) : 0;
   t.n = max(t.dx, t.dW);
   return t;
 }
@@ -184,7 +184,7 @@ size_t linear_ws_bytes(int M, int K, int N) { return pack_bytes(M, K) + pack_byt
 
 size_t linear_bwd_ws_bytes(int M, int K, int N) {
   return up256((size_t)cdiv(M, dact_rows(M)) * N * 4) + 3 * up256((size_t)M * pad8(N) * 2) + pack_bytes(M, K) +
-         pack_bytes(K, N);
+         pack_bytes(K, N) + gemm_ws_bytes(K, N);
 }
 
 cudaError_t launch_linear(const LinearArgs& a, void* ws, cudaStream_t s) {
@@ -243,6 +243,7 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, void* ws, cudaStream_t s) 
     p.M = a.K; p.N = a.N; p.K = a.M;
     p.ep.out = a.dW;
     p.ep.out_f32 = a.dW_f32;
+    p.ws = at;
     return launch_gemm(p, s);
   }
   return cudaSuccess;
