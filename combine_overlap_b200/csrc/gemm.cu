@@ -18,7 +18,9 @@
 // The tensor cores truncate as they add a product to an accumulator, so a sum's error
 // grows with the number of MMAs in its chain.  Outputs in fp32 (PROMO) therefore leave
 // the accumulator every `chunk` k-blocks and are summed on in registers, rounded to
-// nearest.  bf16 outputs, whose last rounding is far larger, keep one chain.
+// nearest; the lower terms of B have accumulator columns of their own, so that they add
+// nothing to the chain of the highest.  bf16 outputs, whose last rounding is far larger,
+// keep one chain.
 #include "gemm.cuh"
 
 #include <string.h>
@@ -31,6 +33,7 @@ constexpr int G_THREADS = 320;            // warp 0 TMA, warp 1 MMA, warps 2-9 e
 constexpr int G_EPI = 8;
 constexpr int G_MAX_NST = 12;
 constexpr int A_BYTES = 16384;            // a CTA's A tile of a k-block: 128 rows x 64 bf16
+constexpr int LOW_COLS = 128;             // where an accumulator keeps the lower terms' products
 constexpr int G_RING = 196608;            // bytes of the operand ring
 constexpr int G_STAGING = G_EPI * 4096;   // per epilogue warp: 32 rows x 32 fp32 columns
 constexpr double G_FILL = 50.0;           // see cost()
@@ -57,10 +60,11 @@ struct GemmArgs {
   int BN;                                 // columns per tile, a multiple of 16, <= 256
   int S, SW;                              // split of the reduction: in a cluster, in slices
   int PB;                                 // planes of B
-  int nst, stage_bytes, kb_bytes;         // ring; bytes of a stage and of a k-block in it
-  int b_bytes;                            // bytes of one CTA's tile of a B plane
-  int b_boxes;                            // B, n contiguous: 64-column boxes per CTA and plane
+  int nst, stage_bytes;                   // ring
   int kps;                                // k-blocks of 64 per stage
+  int b_bytes;                            // a stage's bytes of one plane of one CTA's B tile
+  int b_boxes;                            // B, n contiguous: 64-column atoms per CTA and plane
+  int a_whole, b_whole;                   // one copy brings all of a stage's A (B)
   int chunk;                              // k-blocks per accumulator chain, a multiple of kps
   int group;                              // row tiles per raster group
   int tma_out, tma_pre;                   // rows of 16-byte multiples: chunks leave by TMA
@@ -101,6 +105,14 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
   return p != 0;
+}
+
+__device__ __forceinline__ void tma_load_4d_pair(void* dst, const void* tmap, uint32_t bar_cluster, int c0, int c1,
+                                                 int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];"
+      :: "r"(smem_u32(dst)), "l"(tmap), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2), "r"(c3) : "memory");
 }
 
 template <int CG>
@@ -468,7 +480,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
     uint32_t ph = 0;
     bool ok = true;
     const int kps = keep(a.kps), nst = keep(a.nst), PB = keep(a.PB), boxes = keep(a.b_boxes);
-    const int b_bytes = keep(a.b_bytes), stage_bytes = keep(a.stage_bytes), bytes = CG * (A_BYTES + PB * b_bytes);
+    const int b_bytes = keep(a.b_bytes), stage_bytes = keep(a.stage_bytes);
+    const int a_whole = keep(a.a_whole), b_whole = keep(a.b_whole);
     uint8_t* const ring = keep(smem);
     const CUtensorMap *ma = keep(&tm_a), *mb = keep(&tm_b);
     for (int t = t0; t < units && ok; t += tstep) {
@@ -480,28 +493,35 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
         if (elect_one()) {
           uint64_t* fb = &ctl->full[stage];
           const uint32_t fbl = CG == 2 ? mapa_shared(smem_u32(fb), (uint32_t)lead) : 0u;
-          const int n = min(kps, kb1 - kb);
-          if (rank == 0) mbar_arrive_expect_tx(fb, (uint32_t)(bytes * n));
-          auto load = [&](void* d, const CUtensorMap* m, int x, int y, int p) {
-            if (CG == 2) tma_load_3d_pair(d, m, fbl, x, y, p);
-            else tma_load_3d(d, m, fb, x, y, p);
+          if (rank == 0) mbar_arrive_expect_tx(fb, (uint32_t)(CG * stage_bytes));
+          auto load = [&](void* d, const CUtensorMap* m, int x, int y, int z, int p) {
+            if (CG == 2) tma_load_4d_pair(d, m, fbl, x, y, z, p);
+            else tma_load_4d(d, m, fb, x, y, z, p);
           };
           uint8_t* d = ring + stage * stage_bytes;
-          for (int k = kb * 64; k < (kb + n) * 64; k += 64) {
-            if constexpr (AMN) {
-              load(d, ma, m0, k, 0);
-              load(d + 8192, ma, m0 + 64, k, 0);
+          const int k = kb * 64;
+          if constexpr (AMN) {
+            if (a_whole) {
+              load(d, ma, 0, k, m0 >> 6, 0);
             } else {
-              load(d, ma, k, m0, 0);
+              load(d, ma, m0, k, 0, 0);
+              load(d + kps * 8192, ma, m0 + 64, k, 0, 0);
             }
-            d += A_BYTES;
-            for (int p = 0; p < PB; ++p, d += b_bytes) {
-              if constexpr (BMN) {
-                for (int j = 0; j < boxes; ++j) load(d + j * 8192, mb, n0 + j * 64, k, p);
-              } else {
-                load(d, mb, k, n0, p);
-              }
-            }
+          } else {
+            if (a_whole) load(d, ma, 0, m0, kb, 0);
+            else
+              for (int i = 0; i < kps; ++i) load(d + i * A_BYTES, ma, k + i * 64, m0, 0, 0);
+          }
+          d += kps * A_BYTES;
+          if constexpr (BMN) {
+            if (b_whole) load(d, mb, 0, k, n0 >> 6, 0);
+            else
+              for (int p = 0; p < PB; ++p)
+                for (int j = 0; j < boxes; ++j, d += kps * 8192) load(d, mb, n0 + j * 64, k, 0, p);
+          } else {
+            if (b_whole) load(d, mb, 0, n0, kb, 0);
+            else
+              for (int i = 0, step = b_bytes / kps; i < kps; ++i, d += step) load(d, mb, k + i * 64, n0, 0, 0);
           }
         }
         __syncwarp();
@@ -523,13 +543,15 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
       if (CG == 2) tc_commit_pair(bar, mask);
       else tc_commit(bar);
     };
-    // Descriptors of the first stage; 16 of k further on: 32 bytes in a K-major row, 16
-    // rows of 128 bytes otherwise (the address field is in units of 16 bytes)
-    constexpr uint64_t KA = AMN ? 128 : 2, KB = BMN ? 128 : 2;
-    const uint64_t ad0 = smem_desc_sw128(smem_u32(smem), AMN ? 8192 : 16, 1024);
-    const uint64_t bd0 = smem_desc_sw128(smem_u32(smem) + A_BYTES, BMN ? 8192 : 16, 1024);
     const int kps = keep(a.kps), nst = keep(a.nst), PB = keep(a.PB), chunk = keep(a.chunk), K = keep(a.K);
-    const int stage16 = keep(a.stage_bytes >> 4), kb16 = keep(a.kb_bytes >> 4), b16 = keep(a.b_bytes >> 4);
+    // Descriptors of the first stage.  16 of k further on: 32 bytes in a K-major row, 16 rows
+    // of 128 bytes otherwise; the next k-block: the next tile, or 64 rows (the address field
+    // is in units of 16 bytes)
+    constexpr uint64_t KA = AMN ? 128 : 2, KB = BMN ? 128 : 2;
+    const uint64_t ad0 = smem_desc_sw128(smem_u32(smem), AMN ? kps * 8192 : 16, 1024);
+    const uint64_t bd0 = smem_desc_sw128(smem_u32(smem) + kps * A_BYTES, BMN ? kps * 8192 : 16, 1024);
+    const int stage16 = keep(a.stage_bytes >> 4), b16 = keep(a.b_bytes >> 4);
+    const int xkb = AMN ? 512 : A_BYTES >> 4, ykb = keep(BMN ? 512 : (a.b_bytes / a.kps) >> 4);
     int stage = 0, acc = 0;
     uint32_t ph = 0, aph = 0;
     bool ok = true;
@@ -549,29 +571,30 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
           uint64_t x = ad0 + (uint64_t)(stage * stage16), y = bd0 + (uint64_t)(stage * stage16);
           if (K - kb * 64 <= n * 64 - 16) {
             // the last k-block, not all of it there
-            for (int i = 0; i < n; ++i, x += kb16, y += kb16) {
+            for (int i = 0; i < n; ++i, x += xkb, y += ykb) {
               const int ks = min(4, cdiv(K - (kb + i) * 64, 16));
               for (int pb = 0; pb < PB; ++pb)
                 for (int k = 0; k < ks; ++k)
-                  mma<CG>(dt, x + k * KA, y + pb * b16 + k * KB, idesc, i || pb || k ? 1u : more);
+                  mma<CG>(dt + (pb ? LOW_COLS : 0), x + k * KA, y + pb * b16 + k * KB, idesc, i || pb > 1 || k ? 1u : more);
             }
           } else if (PB == 1) {
             mma<CG>(dt, x, y, idesc, more);
 #pragma unroll
             for (int k = 1; k < 4; ++k) mma<CG>(dt, x + k * KA, y + k * KB, idesc, 1u);
             for (int i = 1; i < n; ++i) {
-              x += kb16;
-              y += kb16;
+              x += xkb;
+              y += ykb;
 #pragma unroll
               for (int k = 0; k < 4; ++k) mma<CG>(dt, x + k * KA, y + k * KB, idesc, 1u);
             }
           } else {
-            for (int i = 0; i < n; ++i, x += kb16, y += kb16)
+            for (int i = 0; i < n; ++i, x += xkb, y += ykb)
               for (int pb = 0; pb < PB; ++pb) {
                 const uint64_t z = y + (uint64_t)(pb * b16);
-                mma<CG>(dt, x, z, idesc, i || pb ? 1u : more);
+                const uint32_t dp = dt + (pb ? LOW_COLS : 0);
+                mma<CG>(dp, x, z, idesc, i || pb > 1 ? 1u : more);
 #pragma unroll
-                for (int k = 1; k < 4; ++k) mma<CG>(dt, x + k * KA, z + k * KB, idesc, 1u);
+                for (int k = 1; k < 4; ++k) mma<CG>(dp, x + k * KA, z + k * KB, idesc, 1u);
               }
           }
           commit(&ctl->empty[stage]);
@@ -599,6 +622,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
     uint32_t aph = 0;
     Epilogue ep = load_epilogue<PROMO>(a, tm_out, tm_pre, lane, staging + (warp - 2) * 4096);
     const int BN = keep(a.BN);
+    const bool low = a.PB > 1;
     bool ok = true;
     auto release = [&](int i) {
       tc_fence_before();
@@ -624,20 +648,43 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
         }
       }
       float sum[PROMO ? 4 : 1][32];
+      // sum (+)= this warp's chunks of the accumulator at `tb`
+      auto promote = [&](uint32_t tb, bool first) {
+#pragma unroll
+        for (int i = 0; i < (PROMO ? 4 : 0); ++i) {
+          const int ch = chunk_of(half, i);
+          if (ch * 32 < BN) {
+            uint32_t r[32];
+            tmem_ld32(tb + ch * 32, r);
+            tmem_ld_wait();
+            if (first) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) sum[i][j] = __uint_as_float(r[j]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) sum[i][j] += __uint_as_float(r[j]);
+            }
+          }
+        }
+        if (low) {                        // BN <= 128
+#pragma unroll
+          for (int i = 0; i < (PROMO ? 2 : 0); ++i) {
+            const int ch = chunk_of(half, i);
+            if (ch * 32 < BN) {
+              uint32_t r[32];
+              tmem_ld32(tb + LOW_COLS + ch * 32, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) sum[i][j] += __uint_as_float(r[j]);
+            }
+          }
+        }
+      };
       if constexpr (PROMO) {
         for (int c = 0; c + 1 < nch && ok; ++c) {
           if (!g_wait<CG>(&ctl->tfull[acc], aph, ctl)) { ok = false; break; }
           tc_fence_after();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int ch = chunk_of(half, i);
-            if (ch * 32 >= BN) break;
-            uint32_t r[32];
-            tmem_ld32(lanes + (uint32_t)(acc * ACC_COLS + ch * 32), r);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) sum[i][j] = c ? sum[i][j] + __uint_as_float(r[j]) : __uint_as_float(r[j]);
-          }
+          promote(lanes + (uint32_t)(acc * ACC_COLS), c == 0);
           release(acc);
           acc ^= 1;
           if (acc == 0) aph ^= 1u;
@@ -647,18 +694,18 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
       tc_fence_after();
       const uint32_t tb = lanes + (uint32_t)(acc * ACC_COLS);
       if constexpr (PROMO) {
-        if (nch > 1) {
+        if (nch > 1 || low) {
           // the last chain joins the sums, and the sums go where the code below reads
+          promote(tb, nch == 1);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int ch = chunk_of(half, i);
-            if (ch * 32 >= BN) break;
-            uint32_t r[32];
-            tmem_ld32(tb + ch * 32, r);
-            tmem_ld_wait();
+            if (ch * 32 < BN) {
+              uint32_t r[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(sum[i][j] + __uint_as_float(r[j]));
-            tmem_st32(tb + ch * 32, r);
+              for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(sum[i][j]);
+              tmem_st32(tb + ch * 32, r);
+            }
           }
           tmem_st_wait();
         }
@@ -731,15 +778,23 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// {inner, outer, planes}: boxes of 64 inner elements x box_rows, 128-byte swizzle; what
-// lies outside reads as zero.
-bool encode3(CUtensorMap* m, const GemmOperand& o, int inner, int outer, int box_rows) {
+// An operand of `inner` contiguous elements x `outer` rows: 128-byte rows of 64 elements,
+// 128-byte swizzle; what lies outside reads as zero.  whole: {64, outer, inner / 64, planes}
+// (inner a multiple of 64) in boxes of `rows` rows, `blocks` 64-element blocks and
+// `planes` planes, or else {inner, outer, 1, planes} in boxes of one block of one plane.
+// Copies cost about 0.1 us of the copy unit each, whatever their size, so a stage is
+// brought by as few as can be: the up
+// projection of 4096 x 4096 x 14336 takes 311 us with whole boxes, 344 us with one
+// per 64 columns.
+bool encode4(CUtensorMap* m, const GemmOperand& o, int inner, int outer, int rows, bool whole, int blocks, int planes) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, (cuuint64_t)o.planes};
-  const cuuint64_t strides[2] = {(cuuint64_t)o.ld, (cuuint64_t)(o.planes > 1 ? o.plane : o.ld * (size_t)outer)};
-  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, es[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.p), dims, strides, box, es,
+  const cuuint64_t dims[4] = {(cuuint64_t)(whole ? 64 : inner), (cuuint64_t)outer, (cuuint64_t)(whole ? inner / 64 : 1),
+                              (cuuint64_t)o.planes};
+  const cuuint64_t strides[3] = {(cuuint64_t)o.ld, 128, (cuuint64_t)(o.planes > 1 ? o.plane : 128)};
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, (cuuint32_t)(whole ? blocks : 1), (cuuint32_t)(whole ? planes : 1)};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(o.p), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -795,7 +850,8 @@ cudaError_t run_major(const GemmProblem& p, const CUtensorMap (&m)[4], const Gem
 
 // SM cycles of one tile configuration, from rates measured on one B200: an MMA of
 // 128 (per CTA) x BN x 16 takes BN / 2 cycles, and a stage's bytes arrive at no more than
-// FILL per cycle and SM; a tile's epilogue is hidden but for the last.
+// FILL per cycle and SM; a tile's epilogue is hidden but for the last, and a pair's two
+// CTAs cost a tile some cycles to keep in step.
 struct Shape { int CG, BN, S, SW; };
 
 // Clusters of `size` CTAs that a device holds at once (one CTA per SM): fewer than SMs /
@@ -837,8 +893,8 @@ double cost(const GemmProblem& p, int dev, int nsm, Shape c) {
   const int waves = cdiv(units, clusters_of(dev, nsm, c.CG * c.S));
   double tail = 2500.0 + 8.0 * c.BN + (c.CG > 1 ? 800.0 : 0.0);
   if (c.S > 1) tail += 2500.0 + 16.0 * c.BN;
-  if (c.SW > 1) tail += 6000.0 + c.SW * (double)p.M * p.N * 8.0 / (nsm * 20.0);
-  return waves * (cdiv(nkb, c.S * c.SW) * kb + 300.0) + tail;
+  if (c.SW > 1) tail += 3500.0 + c.SW * (double)p.M * p.N * 8.0 / (nsm * 40.0);
+  return waves * (cdiv(nkb, c.S * c.SW) * kb + (c.CG > 1 ? 1500.0 : 300.0)) + tail;
 }
 
 // BN is a multiple of 32, so that a chunk of the epilogue lies in one tile, or 16 for N <= 16.
@@ -939,19 +995,24 @@ cudaError_t launch_gemm(const GemmProblem& p, cudaStream_t s) {
   a.tiles_n = cdiv(p.N, a.BN);
   const int ntiles = a.tiles_m * a.tiles_n, cols = a.BN / c.CG;
   a.b_boxes = cdiv(cols, 64);
-  a.b_bytes = p.b_mn ? a.b_boxes * 8192 : cols * 128;
-  // the ring's tiles start on 1024-byte boundaries (cols is a multiple of 8)
-  a.kb_bytes = A_BYTES + a.PB * a.b_bytes;
-  a.kps = a.kb_bytes <= 24576 ? 2 : 1;
-  a.stage_bytes = a.kps * a.kb_bytes;
+  const int b_kb = p.b_mn ? a.b_boxes * 8192 : cols * 128;   // one k-block of one plane
+  // the ring's tiles start on 1024-byte boundaries (cols is a multiple of 16)
+  a.kps = A_BYTES + a.PB * b_kb <= 24576 ? 2 : 1;
+  a.b_bytes = a.kps * b_kb;
+  a.stage_bytes = a.kps * A_BYTES + a.PB * a.b_bytes;
+  a.a_whole = (p.a_mn ? p.M : p.K) % 64 == 0;
+  a.b_whole = p.b_mn ? p.N % 64 == 0 && cols % 64 == 0 : p.K % 64 == 0;
   a.nst = min(G_MAX_NST, G_RING / a.stage_bytes);
   a.group = c.CG == 2 ? 8 : 16;
   // 32 MMAs in a chain keep an fp32 output within 1e-6 of the exact sum
   const bool promo = p.ep.out_f32 || a.SW > 1;
-  a.chunk = p.ep.out_f32 ? max(1, 8 / a.PB) : 1 << 30;
+  a.chunk = p.ep.out_f32 ? 8 : 1 << 30;
   CUtensorMap m[4];
-  if (!(p.a_mn ? encode3(&m[0], p.A, p.M, p.K, 64) : encode3(&m[0], p.A, p.K, p.M, 128))) return cudaErrorInvalidValue;
-  if (!(p.b_mn ? encode3(&m[1], p.B, p.N, p.K, 64) : encode3(&m[1], p.B, p.K, p.N, cols))) return cudaErrorInvalidValue;
+  if (!(p.a_mn ? encode4(&m[0], p.A, p.M, p.K, 64 * a.kps, a.a_whole, 2, 1)
+               : encode4(&m[0], p.A, p.K, p.M, 128, a.a_whole, a.kps, 1)) ||
+      !(p.b_mn ? encode4(&m[1], p.B, p.N, p.K, 64 * a.kps, a.b_whole, a.b_boxes, a.PB)
+               : encode4(&m[1], p.B, p.K, p.N, cols, a.b_whole, a.kps, 1)))
+    return cudaErrorInvalidValue;
   a.tma_out = a.S == 1 && p.N % (p.ep.out_f32 ? 4 : 8) == 0;
   a.tma_pre = a.S == 1 && p.ep.pre && p.N % 8 == 0;
   m[2] = m[3] = m[0];                     // read with tma_out, tma_pre only

@@ -5,13 +5,13 @@
 
 namespace moe {
 
-// C [M][N] = epilogue( sum over planes pa, pb and over k of A_pa(m, k) B_pb(k, n) ).
+// C [M][N] = epilogue( sum over B's planes p and over k of A(m, k) B_p(k, n) ).
 // An operand is `planes` bf16 matrices, `plane` bytes apart, of rows `ld` bytes apart
-// (a multiple of 16; base 16-byte aligned):
-//   A: [M][K] (k contiguous) or, a_mn set, [K][M] (m contiguous)
-//   B: [K][N] (n contiguous, b_mn set) or [N][K] (k contiguous)
+// (multiples of 16; base 16-byte aligned):
+//   A: [M][K] (k contiguous) or, a_mn set, [K][M] (m contiguous); its first plane counts
+//   B: [K][N] (n contiguous, b_mn set) or [N][K] (k contiguous; one plane)
 // Planes are the bf16 terms of an operand of more than 8 bits; each stage of the
-// operand ring holds all of them, so the other operand is read once for all.
+// operand ring holds all of them, so A is read once for all.
 struct GemmOperand {
   const void* p;
   size_t ld, plane;

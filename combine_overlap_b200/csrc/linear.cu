@@ -69,13 +69,14 @@ cudaError_t pack(const void* in, long rows, int n, char** at, GemmOperand* o, cu
 size_t pack_bytes(long rows, int n) { return n % 8 ? up256((size_t)rows * pad8(n) * 2) : 0; }
 
 // ------------------------------------------------------------------- dact ---
-// A block takes 128 columns (16 threads of 8) and `rows` rows, 16 at a time.  du's
-// planes: plane 0 = bf16(du), plane p = bf16(du - the earlier planes).  `part`
+// A block takes 128 columns (16 threads of 8) and `rows` rows, 16 at a time.  du's terms
+// stand side by side in a row of its own: term 0 = bf16(du), term p = bf16(du - the
+// earlier terms), n8 columns each.  `part`
 // [gridDim.y][N] (optional): the block's column sums, in a fixed order.
 __global__ void __launch_bounds__(256) dact_kernel(const void* __restrict__ dout, int f32,
                                                    const __nv_bfloat16* __restrict__ pre, int act, int M,
                                                    int N, int rows, int planes, __nv_bfloat16* __restrict__ du,
-                                                   size_t plane, int n8, float* __restrict__ part) {
+                                                   int n8, float* __restrict__ part) {
   pdl_trigger();
   pdl_wait();
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(256) dact_kernel(const void* __restrict__ dout
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-        *reinterpret_cast<uint4*>(du + p * plane + (size_t)m * n8 + n) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(du + ((size_t)m * planes + p) * n8 + n) = make_uint4(w[0], w[1], w[2], w[3]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xffff0000u);
@@ -205,14 +206,14 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, void* ws, cudaStream_t s) 
   float* part = reinterpret_cast<float*>(at);
   at += up256((size_t)nblk * a.N * 4);
   const Terms t = terms_of(a);
-  GemmOperand du = {at, (size_t)n8 * 2, up256((size_t)a.M * n8 * 2), t.n};
-  at += 3 * du.plane;
+  GemmOperand du = {at, (size_t)t.n * n8 * 2, (size_t)n8 * 2, t.n};
+  at += 3 * up256((size_t)a.M * n8 * 2);
   // dout is an operand as it stands if it is bf16, unpadded and without an activation
   const bool direct = !a.dout_f32 && !a.act && n8 == a.N;
   if (!direct || a.dbias) {
     cudaError_t e = launch_pdl(dact_kernel, dim3(cdiv(n8, 128), nblk), dim3(256), 0, s, a.dout, a.dout_f32,
                                static_cast<const __nv_bfloat16*>(a.pre), a.act, a.M, a.N, rows,
-                               direct ? 0 : t.n, (__nv_bfloat16*)du.p, du.plane / 2, n8,
+                               direct ? 0 : t.n, (__nv_bfloat16*)du.p, n8,
                                a.dbias ? part : nullptr);
     if (e != cudaSuccess) return e;
   }
