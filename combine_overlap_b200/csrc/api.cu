@@ -525,9 +525,7 @@ moe_status moe_route_scored_backward(const float* dgate, const float* logits, co
   s = check_router(router, E, k, &r);
   if (s != MOE_OK) return s;
   if (!ok_ptr(dgate) || !ok_ptr(logits) || !ok_ptr(topk_idx) || !ok_ptr(dlogits)) return MOE_ERR_INVALID;
-  const int nsm = device_sms();
-  if (nsm <= 0) return cuda_fail(cudaErrorInvalidDevice);
-  return cuda_status(launch_route_scored_bwd(dgate, logits, topk_idx, T, E, k, r, dlogits, nsm,
+  return cuda_status(launch_route_scored_bwd(dgate, logits, topk_idx, T, E, k, r, dlogits,
                                              static_cast<cudaStream_t>(stream)));
 }
 
@@ -538,11 +536,9 @@ moe_status moe_combine_backward(const void* dout, const void* y, const int32_t* 
   if (k > MAX_K || d % 8 != 0 || (long long)T * k > (1LL << 30)) return MOE_ERR_UNSUPPORTED;
   if (!ok_ptr(dout) || !ok_ptr(y) || !ok_ptr(row_of) || !ok_ptr(topk_gate) || !ok_opt(dy) || !ok_ptr(dgate))
     return MOE_ERR_INVALID;
-  const int nsm = device_sms();
-  if (nsm <= 0) return cuda_fail(cudaErrorInvalidDevice);
   return cuda_status(launch_combine_bwd(static_cast<const __nv_bfloat16*>(dout),
                                         static_cast<const __nv_bfloat16*>(y), row_of, topk_gate, T, d, k,
-                                        static_cast<__nv_bfloat16*>(dy), dgate, nsm,
+                                        static_cast<__nv_bfloat16*>(dy), dgate,
                                         static_cast<cudaStream_t>(stream)));
 }
 

@@ -975,13 +975,27 @@ size_t gemm_ws_bytes(int M, int N) {
   return n > 1 ? (size_t)n * M * (cdiv(N, 4) * 4) * 4 : 0;
 }
 
+cudaError_t device_of(int* dev, int* sms) {
+  static int count[64] = {0};
+  int d = 0;
+  cudaError_t e = cudaGetDevice(&d);
+  if (e != cudaSuccess) return e;
+  if (d < 0 || d >= 64) return cudaErrorInvalidDevice;
+  if (count[d] == 0) {
+    int n = 0;
+    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d);
+    if (e != cudaSuccess) return e;
+    count[d] = n;
+  }
+  if (dev) *dev = d;
+  *sms = count[d];
+  return cudaSuccess;
+}
+
 cudaError_t launch_gemm(const GemmProblem& p, cudaStream_t s) {
   int dev = 0, nsm = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  cudaError_t e = device_of(&dev, &nsm);
   if (e != cudaSuccess) return e;
-  e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   GemmArgs a;
   memset(&a, 0, sizeof(a));
   a.M = p.M; a.N = p.N; a.K = p.K;

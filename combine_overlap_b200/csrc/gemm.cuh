@@ -27,6 +27,9 @@ struct GemmProblem {
                                  // with an output alone (no bias, activation, residual, pre)
 };
 
+// The current device and its SMs (asked of the driver once per device).
+cudaError_t device_of(int* dev, int* sms);
+
 size_t gemm_ws_bytes(int M, int N);
 int gemm_slices(int M, int N);
 cudaError_t launch_gemm(const GemmProblem& p, cudaStream_t s);

@@ -129,12 +129,12 @@ cudaError_t launch_route_scored(const float* logits, int T, int E, int k, const 
                                 uint32_t* arrive_or_null, uint32_t* ready_q_or_null, cudaStream_t s);
 cudaError_t launch_route_scored_bwd(const float* dgate, const float* logits, const int32_t* topk_idx,
                                     int T, int E, int k, const RouterArgs& r, float* dlogits,
-                                    int num_sms, cudaStream_t s);
+                                    cudaStream_t s);
 
 // combine_bwd.cu
 cudaError_t launch_combine_bwd(const __nv_bfloat16* dout, const __nv_bfloat16* y, const int32_t* row_of,
                                const float* gate, int T, int d, int k, __nv_bfloat16* dy_or_null,
-                               float* dgate, int num_sms, cudaStream_t s);
+                               float* dgate, cudaStream_t s);
 
 // linear.cu
 struct LinearEpi {
@@ -160,6 +160,7 @@ struct LinearBwdArgs {
 size_t linear_ws_bytes(int M, int K, int N);
 size_t linear_bwd_ws_bytes(int M, int K, int N);
 cudaError_t launch_linear(const LinearArgs& a, void* ws, cudaStream_t s);
+cudaError_t launch_linear_small(const LinearArgs& a, int num_sms, cudaStream_t s);   // linear_small.cu: M <= 8
 cudaError_t launch_linear_bwd(const LinearBwdArgs& a, void* ws, cudaStream_t s);
 // gemm.cu: synchronises s; *word = 1 if a wait of a product ran out since the last call.
 cudaError_t linear_timeout(cudaStream_t s, uint32_t* word);

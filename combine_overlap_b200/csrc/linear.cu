@@ -17,10 +17,10 @@ __device__ __forceinline__ float dact_f32(int act, float u) {
   switch (act) {
     case 1: return u > 0.0f ? 1.0f : 0.0f;
     case 2: {
-      const float p = 1.0f / (1.0f + expf(-u));
+      const float p = __fdividef(1.0f, 1.0f + __expf(-u));
       return p * (1.0f + u * (1.0f - p));
     }
-    case 3: return 0.5f * (1.0f + erff(u * 0.70710678f)) + u * expf(-0.5f * u * u) * 0.39894228f;
+    case 3: return 0.5f * (1.0f + erff(u * 0.70710678f)) + u * __expf(-0.5f * u * u) * 0.39894228f;
   }
   return 1.0f;
 }
@@ -73,8 +73,28 @@ size_t pack_bytes(long rows, int n) { return n % 8 ? up256((size_t)rows * pad8(n
 // stand side by side in a row of its own: term 0 = bf16(du), term p = bf16(du - the
 // earlier terms), n8 columns each.  `part`
 // [gridDim.y][N] (optional): the block's column sums, in a fixed order.
+// What bounds it is memory: R rows' loads are in flight per thread.
+constexpr int DACT_R = 4;
+
+__device__ __forceinline__ void dact_load(const void* __restrict__ dout, int f32, size_t at, int n, int N, bool vec,
+                                          float (&v)[8]) {
+  if (!vec) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = n + i >= N ? 0.0f : f32 ? static_cast<const float*>(dout)[at + i]
+                                     : __bfloat162float(static_cast<const __nv_bfloat16*>(dout)[at + i]);
+  } else if (f32) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(dout) + at));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(dout) + at) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(dout) + at)), v);
+  }
+}
+
+template <int ACT>
 __global__ void __launch_bounds__(256) dact_kernel(const void* __restrict__ dout, int f32,
-                                                   const __nv_bfloat16* __restrict__ pre, int act, int M,
+                                                   const __nv_bfloat16* __restrict__ pre, int M,
                                                    int N, int rows, int planes, __nv_bfloat16* __restrict__ du,
                                                    int n8, float* __restrict__ part) {
   pdl_trigger();
@@ -85,44 +105,37 @@ __global__ void __launch_bounds__(256) dact_kernel(const void* __restrict__ dout
   const int m1 = min(M, (int)(blockIdx.y + 1) * rows);
   float sum[8] = {};
   if (n < n8) {
-    for (int m = blockIdx.y * rows + ty; m < m1; m += 16) {
-      const size_t at = (size_t)m * N + n;
-      float v[8] = {}, u[8] = {};
-      if (vec) {
-        if (f32) {
-          const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(dout) + at));
-          const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(dout) + at) + 1);
-          v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        } else {
-          bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(dout) + at)), v);
+    for (int m0 = blockIdx.y * rows + ty; m0 < m1; m0 += 16 * DACT_R) {
+      float v[DACT_R][8], u[ACT ? DACT_R : 1][8];
+#pragma unroll
+      for (int r = 0; r < DACT_R; ++r) {
+        const int m = m0 + 16 * r;
+        if (m < m1) {
+          dact_load(dout, f32, (size_t)m * N + n, n, N, vec, v[r]);
+          if (ACT) dact_load(pre, 0, (size_t)m * N + n, n, N, vec, u[ACT ? r : 0]);
         }
-        if (act) bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(pre + at)), u);
-      } else {
+      }
+#pragma unroll
+      for (int r = 0; r < DACT_R; ++r) {
+        const int m = m0 + 16 * r;
+        if (m >= m1) break;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if (n + i < N) {
-            v[i] = f32 ? static_cast<const float*>(dout)[at + i]
-                       : __bfloat162float(static_cast<const __nv_bfloat16*>(dout)[at + i]);
-            if (act) u[i] = __bfloat162float(pre[at + i]);
-          }
+          if (ACT) v[r][i] *= dact_f32(ACT, u[ACT ? r : 0][i]);
+          sum[i] += v[r][i];
         }
-      }
-      if (act) {
+        for (int p = 0; p < planes; ++p) {
+          uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= dact_f32(act, u[i]);
-      }
+          for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(v[r][2 * i], v[r][2 * i + 1]);
+          *reinterpret_cast<uint4*>(du + ((size_t)m * planes + p) * n8 + n) = make_uint4(w[0], w[1], w[2], w[3]);
+          if (p + 1 == planes) break;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += v[i];
-      for (int p = 0; p < planes; ++p) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-        *reinterpret_cast<uint4*>(du + ((size_t)m * planes + p) * n8 + n) = make_uint4(w[0], w[1], w[2], w[3]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xffff0000u);
-          v[2 * i] = isfinite(lo) ? v[2 * i] - lo : 0.0f;   // an infinity has no remainder
-          v[2 * i + 1] = isfinite(hi) ? v[2 * i + 1] - hi : 0.0f;
+          for (int i = 0; i < 4; ++i) {
+            const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xffff0000u);
+            v[r][2 * i] = isfinite(lo) ? v[r][2 * i] - lo : 0.0f;   // an infinity has no remainder
+            v[r][2 * i + 1] = isfinite(hi) ? v[r][2 * i + 1] - hi : 0.0f;
+          }
         }
       }
     }
@@ -150,8 +163,10 @@ __global__ void __launch_bounds__(256) dbias_kernel(const float* __restrict__ pa
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int n = blockIdx.x * 32 + lane;
   float sum = 0.0f;
-  if (n < N)
+  if (n < N) {
+#pragma unroll 8
     for (int b = w; b < nblk; b += 8) sum += part[(size_t)b * N + n];
+  }
   sh[w][lane] = sum;
   __syncthreads();
   if (w == 0 && n < N) {
@@ -162,9 +177,13 @@ __global__ void __launch_bounds__(256) dbias_kernel(const float* __restrict__ pa
   }
 }
 
-// Rows per dact block: 16 at the least, so that a block has work, and not so few that
-// there are more than 256 blocks of rows.
-int dact_rows(int M) { return max(16, cdiv(cdiv(M, 256), 16) * 16); }
+// Rows per dact block: 16 at the least, so that a block has work; 64, DACT_R loads in
+// flight in each thread, where that leaves blocks for two waves of the device; and not so
+// few that there are more than 256 blocks of rows.
+int dact_rows(int M, int N) {
+  const int most = max(16, cdiv(cdiv(M, 256), 16) * 16);
+  return (long long)cdiv(M, 64) * cdiv(N, 128) >= 600 ? max(64, most) : most;
+}
 
 // The bf16 terms that du goes in as.  bf16 gradients take it rounded once, as a stored
 // bf16 gradient would be: an error of the size of their own rounding.  An fp32 dW takes
@@ -181,14 +200,22 @@ Terms terms_of(const LinearBwdArgs& a) {
 
 }  // namespace
 
-size_t linear_ws_bytes(int M, int K, int N) { return pack_bytes(M, K) + pack_bytes(K, N); }
+// Up to SMALL_M rows go without the tensor cores (linear_small.cu).
+constexpr int SMALL_M = 8;
+
+size_t linear_ws_bytes(int M, int K, int N) { return M <= SMALL_M ? 0 : pack_bytes(M, K) + pack_bytes(K, N); }
 
 size_t linear_bwd_ws_bytes(int M, int K, int N) {
-  return up256((size_t)cdiv(M, dact_rows(M)) * N * 4) + 3 * up256((size_t)M * pad8(N) * 2) + pack_bytes(M, K) +
+  return up256((size_t)cdiv(M, dact_rows(M, N)) * N * 4) + 3 * up256((size_t)M * pad8(N) * 2) + pack_bytes(M, K) +
          pack_bytes(K, N) + gemm_ws_bytes(K, N);
 }
 
 cudaError_t launch_linear(const LinearArgs& a, void* ws, cudaStream_t s) {
+  if (a.M <= SMALL_M) {
+    int nsm = 0;
+    const cudaError_t e = device_of(nullptr, &nsm);
+    return e == cudaSuccess ? launch_linear_small(a, nsm, s) : e;
+  }
   char* at = static_cast<char*>(ws);
   GemmProblem p = {};
   cudaError_t e = pack(a.x, a.M, a.K, &at, &p.A, s);
@@ -202,7 +229,7 @@ cudaError_t launch_linear(const LinearArgs& a, void* ws, cudaStream_t s) {
 
 cudaError_t launch_linear_bwd(const LinearBwdArgs& a, void* ws, cudaStream_t s) {
   char* at = static_cast<char*>(ws);
-  const int rows = dact_rows(a.M), nblk = cdiv(a.M, rows), n8 = pad8(a.N);
+  const int rows = dact_rows(a.M, a.N), nblk = cdiv(a.M, rows), n8 = pad8(a.N);
   float* part = reinterpret_cast<float*>(at);
   at += up256((size_t)nblk * a.N * 4);
   const Terms t = terms_of(a);
@@ -211,8 +238,9 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, void* ws, cudaStream_t s) 
   // dout is an operand as it stands if it is bf16, unpadded and without an activation
   const bool direct = !a.dout_f32 && !a.act && n8 == a.N;
   if (!direct || a.dbias) {
-    cudaError_t e = launch_pdl(dact_kernel, dim3(cdiv(n8, 128), nblk), dim3(256), 0, s, a.dout, a.dout_f32,
-                               static_cast<const __nv_bfloat16*>(a.pre), a.act, a.M, a.N, rows,
+    auto kernel = a.act == 1 ? dact_kernel<1> : a.act == 2 ? dact_kernel<2> : a.act == 3 ? dact_kernel<3> : dact_kernel<0>;
+    cudaError_t e = launch_pdl(kernel, dim3(cdiv(n8, 128), nblk), dim3(256), 0, s, a.dout, a.dout_f32,
+                               static_cast<const __nv_bfloat16*>(a.pre), a.M, a.N, rows,
                                direct ? 0 : t.n, (__nv_bfloat16*)du.p, n8,
                                a.dbias ? part : nullptr);
     if (e != cudaSuccess) return e;

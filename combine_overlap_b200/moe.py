@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 
 import torch
 
@@ -149,8 +150,8 @@ _lib.moe_ep_owner_forward.argtypes = [ctypes.POINTER(EpOwnerArgs), _I, _P, _S, _
 _lib.moe_ep_home_combine.argtypes = [_P, _P, _P, _P, _I, _I, _I, _P, _P, _I, _P]
 _lib.moe_ep_debug_plan.argtypes = [_P, _I, _I, _I, _I, _I, _P, _P, _I]
 _lib.moe_ep_debug_plan.restype = _I
-_lib.moe_route_scored.argtypes = [_P, _I, _I, _I, ctypes.POINTER(RouterArgs), _P, _P, _P, _P, _S, _P]
-_lib.moe_route_scored_backward.argtypes = [_P, _P, _P, _I, _I, _I, ctypes.POINTER(RouterArgs), _P, _P]
+_lib.moe_route_scored.argtypes = [_P, _I, _I, _I, _P, _P, _P, _P, _P, _S, _P]
+_lib.moe_route_scored_backward.argtypes = [_P, _P, _P, _I, _I, _I, _P, _P, _P]
 _lib.moe_layer_forward_scored.argtypes = [ctypes.POINTER(LayerArgs), ctypes.POINTER(RouterArgs), _I, _P,
                                           _S, _P]
 _lib.moe_combine_backward.argtypes = [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P]
@@ -158,8 +159,8 @@ _lib.moe_linear_workspace_size.argtypes = [_I, _I, _I]
 _lib.moe_linear_workspace_size.restype = _S
 _lib.moe_linear_backward_workspace_size.argtypes = [_I, _I, _I]
 _lib.moe_linear_backward_workspace_size.restype = _S
-_lib.moe_linear.argtypes = [ctypes.POINTER(LinearArgs), _P, _S, _P]
-_lib.moe_linear_backward.argtypes = [ctypes.POINTER(LinearBwdArgs), _P, _S, _P]
+_lib.moe_linear.argtypes = [_P, _P, _S, _P]
+_lib.moe_linear_backward.argtypes = [_P, _P, _S, _P]
 _lib.moe_linear_get_status.argtypes = [_P]
 _lib.moe_linear_get_status.restype = _I
 for _fn in ("moe_route_scored", "moe_route_scored_backward", "moe_layer_forward_scored",
@@ -450,34 +451,62 @@ def debug_tokens_combined(ws: torch.Tensor, T: int, d: int, f: int, E: int, k: i
 
 
 # ---- the linear layer, the scored router and their gradients ----------------
+# These calls are short on the device, so their own time on the host counts: arguments go
+# to the library as packed bytes, and a tensor's checks are one pass that falls back to
+# _need for the error's words.
+_LINEAR = struct.Struct("iiiPPPPiiPP")
+_LINEAR_BWD = struct.Struct("iiiPPPPiiiPPP")
+_ROUTER = struct.Struct("iPiiiif0P")
+assert (_LINEAR.size, _LINEAR_BWD.size, _ROUTER.size) == tuple(
+    ctypes.sizeof(c) for c in (LinearArgs, LinearBwdArgs, RouterArgs))
+_BF16, _F32 = torch.bfloat16, torch.float32
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _same_device(*named):
-    """Every given tensor on one device, the current one: the library launches there."""
+    """Every given tensor on one device, the current one: the library launches there.
+    Returns its current stream."""
     cur = torch.cuda.current_device()
     for t, name in named:
         if t is not None and t.get_device() != cur:
             raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{cur}")
+    return _raw_stream(cur)
 
 
 def _dtype_code(dtype, name: str) -> int:
-    if dtype is torch.bfloat16:
+    if dtype is _BF16:
         return DTYPE_BF16
-    if dtype is torch.float32:
+    if dtype is _F32:
         return DTYPE_F32
     raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {dtype}")
 
 
 def _need2(t, dtype, name: str):
+    """The shape of a contiguous 2-D CUDA tensor of dtype."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        shape = t.shape
+        if len(shape) == 2:
+            return shape
     _need(t, dtype, name)
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
+    raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
 
 
-def _scratch(ws, need: int, device, what: str):
+def _given(t, dtype, shape: tuple, name: str) -> int:
+    """The address of a contiguous CUDA tensor of dtype and shape."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous()):
+        _need(t, dtype, name)
+    if t.shape != shape:
+        _shape(t, shape, name)
+    return t.data_ptr()
+
+
+def _scratch(ws, need: int, like, what: str):
     """The caller's workspace, or one from torch's allocator (of the current stream)."""
     if need >= 1 << 62:
         raise MoEError(MOE_ERR_INVALID, what)
     if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        return like.new_empty(need, dtype=torch.uint8) if need else None
     _need(ws, torch.uint8, "ws")
     if ws.numel() < need:
         raise ValueError(f"workspace smaller than {what} for this shape")
@@ -501,30 +530,24 @@ def linear(x, W, bias=None, residual=None, act=ACT_NONE, out_dtype=torch.bfloat1
     if stream is not None:
         with torch.cuda.stream(stream):
             return linear(x, W, bias, residual, act, out_dtype, pre, out, ws)
-    _need2(x, torch.bfloat16, "x")
-    _need2(W, torch.bfloat16, "W")
-    M, K = x.shape
-    N = W.shape[1]
-    _shape(W, (K, N), "W")
+    M, K = _need2(x, _BF16, "x")
+    N = _need2(W, _BF16, "W")[1]
+    w_ptr = _given(W, _BF16, (K, N), "W")
     code = _dtype_code(out_dtype, "out_dtype")
-    if bias is not None:
-        _need(bias, torch.float32, "bias")
-        _shape(bias, (N,), "bias")
-    if residual is not None:
-        _need(residual, out_dtype, "residual")
-        _shape(residual, (M, N), "residual")
+    b_ptr = _given(bias, _F32, (N,), "bias") if bias is not None else 0
+    r_ptr = _given(residual, out_dtype, (M, N), "residual") if residual is not None else 0
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        out = x.new_empty((M, N), dtype=out_dtype)
     else:
-        _need(out, out_dtype, "out")
-        _shape(out, (M, N), "out")
-    u = torch.empty((M, N), dtype=torch.bfloat16, device=x.device) if pre else None
-    ws = _scratch(ws, _lib.moe_linear_workspace_size(M, K, N), x.device, "moe_linear_workspace_size")
-    _same_device((x, "x"), (W, "W"), (bias, "bias"), (residual, "residual"), (out, "out"), (ws, "ws"))
-    a = LinearArgs(M, K, N, x.data_ptr(), W.data_ptr(), None if bias is None else bias.data_ptr(),
-                   None if residual is None else residual.data_ptr(), int(act), code, out.data_ptr(),
-                   None if u is None else u.data_ptr())
-    _check(_lib.moe_linear(ctypes.byref(a), _ptr(ws), 0 if ws is None else ws.numel(), _stream()), "moe_linear")
+        _given(out, out_dtype, (M, N), "out")
+    u = x.new_empty((M, N)) if pre else None
+    ws = _scratch(ws, _lib.moe_linear_workspace_size(M, K, N), x, "moe_linear_workspace_size")
+    st = _same_device((x, "x"), (W, "W"), (bias, "bias"), (residual, "residual"), (out, "out"), (ws, "ws"))
+    a = _LINEAR.pack(M, K, N, x.data_ptr(), w_ptr, b_ptr, r_ptr, act, code, out.data_ptr(),
+                     u.data_ptr() if pre else 0)
+    r = _lib.moe_linear(a, *((None, 0) if ws is None else (ws.data_ptr(), ws.numel())), st)
+    if r:
+        _check(r, "moe_linear")
     return (out, u) if pre else out
 
 
@@ -537,33 +560,29 @@ def linear_backward(dout, x, W, pre=None, act=ACT_NONE, dW_dtype=torch.float32, 
     if stream is not None:
         with torch.cuda.stream(stream):
             return linear_backward(dout, x, W, pre, act, dW_dtype, want_dx, want_dW, want_dbias, ws)
-    _need2(x, torch.bfloat16, "x")
-    _need2(W, torch.bfloat16, "W")
-    M, K = x.shape
-    N = W.shape[1]
-    _shape(W, (K, N), "W")
+    M, K = _need2(x, _BF16, "x")
+    N = _need2(W, _BF16, "W")[1]
+    w_ptr = _given(W, _BF16, (K, N), "W")
     code, dW_code = _dtype_code(dout.dtype, "dout"), _dtype_code(dW_dtype, "dW_dtype")
-    _need(dout, dout.dtype, "dout")
-    _shape(dout, (M, N), "dout")
+    d_ptr = _given(dout, dout.dtype, (M, N), "dout")
+    p_ptr = 0
     if act != ACT_NONE:
         if pre is None:
             raise ValueError("linear_backward needs pre (linear(..., pre=True)) with an activation")
-        _need(pre, torch.bfloat16, "pre")
-        _shape(pre, (M, N), "pre")
+        p_ptr = _given(pre, _BF16, (M, N), "pre")
     else:
         pre = None
-    dev = x.device
-    dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev) if want_dx else None
-    dW = torch.empty((K, N), dtype=dW_dtype, device=dev) if want_dW else None
-    db = torch.empty(N, dtype=torch.float32, device=dev) if want_dbias else None
-    ws = _scratch(ws, _lib.moe_linear_backward_workspace_size(M, K, N), dev,
-                  "moe_linear_backward_workspace_size")
-    _same_device((x, "x"), (W, "W"), (dout, "dout"), (pre, "pre"), (ws, "ws"))
-    p = [None if t is None else t.data_ptr() for t in (pre, dx, dW, db)]
-    a = LinearBwdArgs(M, K, N, dout.data_ptr(), x.data_ptr(), W.data_ptr(), p[0], int(act), code, dW_code,
-                      p[1], p[2], p[3])
-    _check(_lib.moe_linear_backward(ctypes.byref(a), _ptr(ws), 0 if ws is None else ws.numel(), _stream()),
-           "moe_linear_backward")
+    dx = x.new_empty((M, K)) if want_dx else None
+    dW = x.new_empty((K, N), dtype=dW_dtype) if want_dW else None
+    db = x.new_empty(N, dtype=_F32) if want_dbias else None
+    ws = _scratch(ws, _lib.moe_linear_backward_workspace_size(M, K, N), x, "moe_linear_backward_workspace_size")
+    st = _same_device((x, "x"), (W, "W"), (dout, "dout"), (pre, "pre"), (ws, "ws"))
+    a = _LINEAR_BWD.pack(M, K, N, d_ptr, x.data_ptr(), w_ptr, p_ptr, act, code, dW_code,
+                         dx.data_ptr() if want_dx else 0, dW.data_ptr() if want_dW else 0,
+                         db.data_ptr() if want_dbias else 0)
+    r = _lib.moe_linear_backward(a, *((None, 0) if ws is None else (ws.data_ptr(), ws.numel())), st)
+    if r:
+        _check(r, "moe_linear_backward")
     return dx, dW, db
 
 
@@ -575,8 +594,7 @@ def linear_get_status(stream=None) -> int:
 
 def _router_args(E, device, score, bias, n_groups, topk_groups, group_score, renorm, scale) -> RouterArgs:
     if bias is not None:
-        _need(bias, torch.float32, "bias")
-        _shape(bias, (E,), "bias")
+        _given(bias, _F32, (E,), "bias")
         if bias.device != device:
             raise ValueError(f"bias is on {bias.device}, the logits on {device}")
     return RouterArgs(int(score), None if bias is None else bias.data_ptr(), int(n_groups), int(topk_groups),
@@ -592,16 +610,18 @@ def route_scored(logits, k: int, score=SCORE_SOFTMAX, bias=None, n_groups=1, top
         with torch.cuda.stream(stream):
             return route_scored(logits, k, score, bias, n_groups, topk_groups, group_score, renorm, scale,
                                 counts, ws)
-    _need2(logits, torch.float32, "logits")
-    T, E = logits.shape
-    dev = logits.device
-    r = _router_args(E, dev, score, bias, n_groups, topk_groups, group_score, renorm, scale)
-    idx = torch.empty((T, k), dtype=torch.int32, device=dev)
-    gate = torch.empty((T, k), dtype=torch.float32, device=dev)
-    cnt = torch.empty(E, dtype=torch.int32, device=dev) if counts else None
-    _same_device((logits, "logits"), (ws, "ws"))
-    _check(_lib.moe_route_scored(_ptr(logits), T, E, k, ctypes.byref(r), _ptr(idx), _ptr(gate), _ptr(cnt),
-                                 _ptr(ws), 0 if ws is None else ws.numel(), _stream()), "moe_route_scored")
+    T, E = _need2(logits, _F32, "logits")
+    b_ptr = _given(bias, _F32, (E,), "bias") if bias is not None else 0
+    idx = logits.new_empty((T, k), dtype=torch.int32)
+    gate = logits.new_empty((T, k))
+    cnt = logits.new_empty(E, dtype=torch.int32) if counts else None
+    st = _same_device((logits, "logits"), (bias, "bias"), (ws, "ws"))
+    r = _lib.moe_route_scored(logits.data_ptr(), T, E, k,
+                              _ROUTER.pack(score, b_ptr, n_groups, topk_groups, group_score, 1 if renorm else 0, scale),
+                              idx.data_ptr(), gate.data_ptr(), cnt.data_ptr() if counts else None,
+                              *((None, 0) if ws is None else (ws.data_ptr(), ws.numel())), st)
+    if r:
+        _check(r, "moe_route_scored")
     return (idx, gate, cnt) if counts else (idx, gate)
 
 
@@ -612,22 +632,20 @@ def route_scored_backward(dgate, logits, topk_idx, score=SCORE_SOFTMAX, renorm=T
     if stream is not None:
         with torch.cuda.stream(stream):
             return route_scored_backward(dgate, logits, topk_idx, score, renorm, scale, dlogits)
-    _need2(logits, torch.float32, "logits")
-    _need2(dgate, torch.float32, "dgate")
-    _need(topk_idx, torch.int32, "topk_idx")
-    T, E = logits.shape
-    k = dgate.shape[1]
-    _shape(dgate, (T, k), "dgate")
-    _shape(topk_idx, (T, k), "topk_idx")
+    T, E = _need2(logits, _F32, "logits")
+    k = _need2(dgate, _F32, "dgate")[1]
+    d_ptr = _given(dgate, _F32, (T, k), "dgate")
+    i_ptr = _given(topk_idx, torch.int32, (T, k), "topk_idx")
     if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=torch.float32, device=logits.device)
+        dlogits = logits.new_empty((T, E))
     else:
-        _need(dlogits, torch.float32, "dlogits")
-        _shape(dlogits, (T, E), "dlogits")
-    _same_device((logits, "logits"), (dgate, "dgate"), (topk_idx, "topk_idx"), (dlogits, "dlogits"))
-    r = _router_args(E, logits.device, score, None, 1, 0, GROUP_MAX, renorm, scale)
-    _check(_lib.moe_route_scored_backward(_ptr(dgate), _ptr(logits), _ptr(topk_idx), T, E, k, ctypes.byref(r),
-                                          _ptr(dlogits), _stream()), "moe_route_scored_backward")
+        _given(dlogits, _F32, (T, E), "dlogits")
+    st = _same_device((logits, "logits"), (dgate, "dgate"), (topk_idx, "topk_idx"), (dlogits, "dlogits"))
+    r = _lib.moe_route_scored_backward(d_ptr, logits.data_ptr(), i_ptr, T, E, k,
+                                       _ROUTER.pack(score, 0, 1, 0, GROUP_MAX, 1 if renorm else 0, scale),
+                                       dlogits.data_ptr(), st)
+    if r:
+        _check(r, "moe_route_scored_backward")
     return dlogits
 
 
@@ -638,24 +656,21 @@ def combine_backward(dout, y, row_of, topk_gate, want_dy=True, dy=None, stream=N
     if stream is not None:
         with torch.cuda.stream(stream):
             return combine_backward(dout, y, row_of, topk_gate, want_dy, dy)
-    _need2(dout, torch.bfloat16, "dout")
-    _need2(y, torch.bfloat16, "y")
-    _need(row_of, torch.int32, "row_of")
-    _need2(topk_gate, torch.float32, "topk_gate")
-    T, k = topk_gate.shape
-    d = y.shape[1]
-    _shape(dout, (T, d), "dout")
-    _shape(y, (T * k, d), "y")
-    _shape(row_of, (T * k,), "row_of")
+    T, k = _need2(topk_gate, _F32, "topk_gate")
+    d = _need2(y, _BF16, "y")[1]
+    y_ptr = _given(y, _BF16, (T * k, d), "y")
+    o_ptr = _given(dout, _BF16, (T, d), "dout")
+    r_ptr = _given(row_of, torch.int32, (T * k,), "row_of")
     if dy is not None:
-        _need(dy, torch.bfloat16, "dy")
-        _shape(dy, (T * k, d), "dy")
+        _given(dy, _BF16, (T * k, d), "dy")
     elif want_dy:
-        dy = torch.empty((T * k, d), dtype=torch.bfloat16, device=y.device)
-    dgate = torch.empty((T, k), dtype=torch.float32, device=y.device)
-    _same_device((dout, "dout"), (y, "y"), (row_of, "row_of"), (topk_gate, "topk_gate"), (dy, "dy"))
-    _check(_lib.moe_combine_backward(_ptr(dout), _ptr(y), _ptr(row_of), _ptr(topk_gate), T, d, k, _ptr(dy),
-                                     _ptr(dgate), _stream()), "moe_combine_backward")
+        dy = y.new_empty((T * k, d))
+    dgate = topk_gate.new_empty((T, k))
+    st = _same_device((dout, "dout"), (y, "y"), (row_of, "row_of"), (topk_gate, "topk_gate"), (dy, "dy"))
+    r = _lib.moe_combine_backward(o_ptr, y_ptr, r_ptr, topk_gate.data_ptr(), T, d, k,
+                                  None if dy is None else dy.data_ptr(), dgate.data_ptr(), st)
+    if r:
+        _check(r, "moe_combine_backward")
     return dy, dgate
 
 
