@@ -26,6 +26,18 @@ __device__ __forceinline__ uint64_t ordered(double f) {
 }
 __device__ __forceinline__ float unordered(uint32_t u) { return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu)); }
 
+// exp(x) and 1 / x, a few units in the last place off; what underflows is 0.
+__device__ __forceinline__ float exp_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
 __device__ __forceinline__ uint64_t warp_max(uint64_t v) {
   const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32));
@@ -39,17 +51,56 @@ __device__ __forceinline__ F warp_sum(F v) {
   return v;
 }
 
+// What a warp has to know, in registers.
+struct Plan {
+  const float *bias, *row;                        // row: the token's logits
+  int E, C, k;                                    // C = ceil(E / 32)
+  int softmax, top2, n_groups, topk_groups;
+  bool grouped, scores;                           // groups limit the choice; p is needed for it
+  int S, L, shift;                                // experts per group; lanes per group, if aligned (or 0)
+};
+__device__ __forceinline__ Plan plan_of(int E, int k, const RouterArgs& o) {
+  Plan p;
+  p.bias = o.bias;
+  p.row = nullptr;
+  p.E = E; p.k = k; p.C = cdiv(E, 32);
+  p.softmax = o.score == 0; p.top2 = o.group_top2;
+  p.n_groups = o.n_groups; p.topk_groups = o.topk_groups;
+  p.grouped = o.topk_groups < o.n_groups;
+  p.scores = o.bias != nullptr || (p.grouped && o.group_top2);
+  p.S = E / o.n_groups;
+  p.L = p.S / p.C;
+  if (p.S % p.C != 0 || (p.L & (p.L - 1)) != 0) p.L = 0;
+  p.shift = p.L ? __ffs(p.L) - 1 : 0;
+  return p;
+}
+
+// A warp's candidates, by id and by rank.
+struct Pool {
+  uint2 found[32], sorted[MAX_K + 1];
+};
+
 // An E-expert row over a warp: lane l holds experts l C .. l C + C - 1, C = ceil(E / 32).
+// CM >= C is its compile-time bound; FULL: E = 32 CM.
 template <int CM>
 struct Row {
   float z[CM];
   uint32_t live, have;                            // bits over i: not masked, exists
 };
 
-template <int CM>
+template <int CM, bool FULL>
 __device__ __forceinline__ void load_row(const float* __restrict__ p, int E, int C, int lane, Row<CM>& r) {
   const int e0 = lane * C;
-  if (CM >= 4 && C == CM && (E & 3) == 0) {
+  if constexpr (FULL && CM == 2) {
+    const float2 v = __ldg(reinterpret_cast<const float2*>(p + e0));
+    r.z[0] = v.x; r.z[1] = v.y;
+  } else if constexpr (FULL && CM >= 4) {
+#pragma unroll
+    for (int i = 0; i < CM / 4; ++i) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(p + e0) + i);
+      r.z[4 * i] = v.x; r.z[4 * i + 1] = v.y; r.z[4 * i + 2] = v.z; r.z[4 * i + 3] = v.w;
+    }
+  } else if (CM >= 4 && C == CM && (E & 3) == 0) {
 #pragma unroll
     for (int i = 0; i < CM / 4; ++i) {
       const float4 v = e0 + 4 * i < E ? __ldg(reinterpret_cast<const float4*>(p + e0) + i) : make_float4(0, 0, 0, 0);
@@ -62,13 +113,13 @@ __device__ __forceinline__ void load_row(const float* __restrict__ p, int E, int
 }
 
 // Sets the masks; a logit of +infinity counts as FLT_MAX, masked ones as 0.
-template <int CM>
+template <int CM, bool FULL>
 __device__ __forceinline__ void mask_row(int E, int C, int lane, Row<CM>& r) {
-  r.live = r.have = 0;
+  r.live = 0;
+  r.have = FULL ? (1u << CM) - 1u : (1u << max(0, min(C, E - lane * C))) - 1u;
 #pragma unroll
   for (int i = 0; i < CM; ++i) {
-    const bool have = i < C && lane * C + i < E, live = have && r.z[i] >= -FLT_MAX;   // not NaN, not -infinity
-    r.have |= have ? 1u << i : 0u;
+    const bool live = (FULL || (r.have >> i & 1u)) && r.z[i] >= -FLT_MAX;   // not NaN, not -infinity
     r.live |= live ? 1u << i : 0u;
     r.z[i] = live ? fminf(r.z[i], FLT_MAX) : 0.0f;
   }
@@ -96,161 +147,311 @@ __device__ __forceinline__ void softmax_row(const Row<CM>& r, float (&ex)[CM], f
   *sum = warp_sum(s);
 }
 
-// One warp chooses one token's experts: lane `slot0 + j` gets slot j's id in *my_e.  Keys
-// and group values are formed in F (float or double) and compared as they are.  In float
-// every decision is checked: a key is within 2^-19 + 2^-22 |key| of its 64-bit value (the
-// scores are at most 1; their sum has 13 roundings at the most, an exponential and a
-// division two each), so two that differ by more than twice that are in the right order; without a bias the keys are the logits themselves, and exact.
-// False: too close to call, the caller has the choice made in double.
-template <typename F, typename U, int CM>
-__device__ bool choose(const Row<CM>& r, int E, int C, int k, const RouterArgs& o, int lane, int slot0, int* my_e) {
-  constexpr bool FAST = sizeof(F) == 4;
-  const bool grouped = o.topk_groups < o.n_groups;
-  const bool scores = o.bias != nullptr || (grouped && o.group_top2);   // p is needed
-  F biased[CM];
-  U key[CM];
-  float reach = 0.0f;                             // the largest |p + bias|
-  if (scores) {
-    if (o.score == 0) {
-      if constexpr (FAST) {
-        float top, sum;
-        softmax_row(r, biased, &top, &sum);
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+// The group limit: bit of each chosen group, from the lanes' values of their groups.
+// `next`: the largest value left out.
+template <typename U>
+__device__ __forceinline__ uint32_t choose_groups(const Plan& o, int lane, U mine, U* last, U* next) {
+  uint32_t chosen = 0;
+  for (int j = 0; j < o.topk_groups; ++j) {
+    *last = warp_max(mine);
+    const int who = __ffs(__ballot_sync(0xffffffffu, mine == *last)) - 1;
+    chosen |= 1u << (who >> o.shift);
+    if (lane == who) mine = 0;
+  }
+  *next = warp_max(mine);
+  return chosen;
+}
+
+// The value of each group, as an ordered key in the lane that speaks for it (lane g << shift
+// for group g), 0 elsewhere.  v: what the groups compare, of this lane's live experts.
+template <typename F>
+struct Two {                                      // the two largest, a >= b
+  F a, b;
+  __device__ __forceinline__ void add(F v) {
+    const F low = a < v ? a : v;
+    b = b > low ? b : low;
+    a = a > v ? a : v;
+  }
+  __device__ __forceinline__ void join(F oa, F ob) {
+    const F low = a < oa ? a : oa, side = b > ob ? b : ob;
+    b = side > low ? side : low;
+    a = a > oa ? a : oa;
+  }
+  // over aligned runs of L lanes
+  __device__ __forceinline__ void join_lanes(int L) {
+    for (int off = 1; off < L; off <<= 1) join(__shfl_xor_sync(0xffffffffu, a, off), __shfl_xor_sync(0xffffffffu, b, off));
+  }
+};
+
+template <typename U, typename F, int CM>
+__device__ __forceinline__ U group_values(const Plan& o, int lane, const F (&v)[CM], uint32_t live, Two<F>* seen) {
+  Two<F> t = {-INFINITY, -INFINITY};
+  U mine = 0;
+  if (o.L) {                                      // groups are aligned runs of L lanes
 #pragma unroll
-        for (int i = 0; i < CM; ++i) biased[i] *= inv;
-      } else {
-        const double top = top_row<CM>(r);
-        double s = 0.0;
+    for (int i = 0; i < CM; ++i) t.add((live >> i & 1u) ? v[i] : -INFINITY);
+    t.join_lanes(o.L);
+    *seen = t;
+    if ((lane & (o.L - 1)) == 0 && (lane >> o.shift) < o.n_groups) mine = ordered(o.top2 && t.b != -INFINITY ? t.a + t.b : t.a);
+    return mine;
+  }
+  for (int g = 0; g < o.n_groups; ++g) {
+    t = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < CM; ++i) {
-          biased[i] = (r.live >> i & 1u) ? exp((double)r.z[i] - top) : 0.0;
-          s += biased[i];
-        }
-        s = warp_sum(s);
-        s = s > 0.0 ? s : 1.0;
+    for (int i = 0; i < CM; ++i) {
+      const int e = lane * o.C + i;
+      if ((live >> i & 1u) && e >= g * o.S && e < g * o.S + o.S) t.add(v[i]);
+    }
+    t.join_lanes(32);
+    if (lane == g) mine = ordered(o.top2 && t.b != -INFINITY ? t.a + t.b : t.a);
+  }
+  return mine;
+}
+
+template <typename U, int CM>
+__device__ __forceinline__ void close_groups(const Plan& o, int lane, uint32_t chosen, U (&key)[CM]) {
 #pragma unroll
-        for (int i = 0; i < CM; ++i) biased[i] /= s;
-      }
-    } else {
+  for (int i = 0; i < CM; ++i) {
+    const int g = o.L ? lane >> o.shift : min(31, (lane * o.C + i) / o.S);
+    if (!(chosen >> g & 1u)) key[i] = 0;
+  }
+}
+
+// One warp chooses one token's experts, every key and group value in 64 bits: lane
+// `slot0 + j` gets slot j's id.  k rounds of a warp-wide largest.
+template <int CM, bool FULL>
+__device__ __noinline__ int choose_f64(const Plan& o, int lane, int slot0, int my_e) {
+  const int C = o.C;
+  Row<CM> r;
+  load_row<CM, FULL>(o.row, o.E, C, lane, r);
+  mask_row<CM, FULL>(o.E, C, lane, r);
+  double v[CM];
+  if (!o.scores) {
+#pragma unroll
+    for (int i = 0; i < CM; ++i) v[i] = (double)r.z[i];
+  } else if (o.softmax) {
+    const double top = top_row<CM>(r);
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < CM; ++i) {
+      v[i] = (r.live >> i & 1u) ? exp((double)r.z[i] - top) : 0.0;
+      sum += v[i];
+    }
+    sum = warp_sum(sum);
+#pragma unroll
+    for (int i = 0; i < CM; ++i) v[i] /= sum > 0.0 ? sum : 1.0;
+  } else {
+#pragma unroll
+    for (int i = 0; i < CM; ++i) v[i] = (r.live >> i & 1u) ? 1.0 / (1.0 + exp(-(double)r.z[i])) : 0.0;
+  }
+  uint64_t key[CM];
+#pragma unroll
+  for (int i = 0; i < CM; ++i) {
+    if (o.bias && (r.have >> i & 1u)) v[i] += (double)__ldg(o.bias + lane * C + i);
+    const double w = o.bias ? v[i] : (double)r.z[i];
+    key[i] = (r.live >> i & 1u) ? ordered(w) : (r.have >> i & 1u) ? 1ull : 0ull;
+  }
+  if (o.grouped) {
+    uint64_t last, next;
+    Two<double> seen;
+    const uint32_t chosen = choose_groups(o, lane, group_values<uint64_t>(o, lane, v, r.live, &seen), &last, &next);
+    close_groups(o, lane, chosen, key);
+  }
+  for (int j = 0; j < o.k; ++j) {
+    uint64_t best = 0;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < CM; ++i)
+      if (key[i] > best) { best = key[i]; at = i; }
+    const uint64_t top = warp_max(best);
+    // lanes hold ascending runs of experts: the lowest lane has the lowest id
+    const int who = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
+    const int e = __shfl_sync(0xffffffffu, lane * C + at, who);
+    if (lane == slot0 + j) my_e = e;
+#pragma unroll
+    for (int i = 0; i < CM; ++i)
+      if (lane == who && i == at) key[i] = 0;
+  }
+  return my_e;
+}
+
+// One token's scores in 64 bits, for a few experts.
+struct Exact {
+  int softmax;
+  double top, sum;
+  __device__ __forceinline__ double score(float z) const {
+    const double e = exp(softmax ? (double)z - top : -(double)z);
+    return softmax ? e / sum : 1.0 / (1.0 + e);
+  }
+};
+template <int CM, bool FULL>
+__device__ __noinline__ Exact exact_of(const float* __restrict__ row, int E, int softmax, int lane) {
+  Exact x = {softmax, 0.0, 1.0};
+  if (softmax) {
+    const int C = cdiv(E, 32);
+    Row<CM> r;
+    load_row<CM, FULL>(row, E, C, lane, r);
+    mask_row<CM, FULL>(E, C, lane, r);
+    x.top = top_row<CM>(r);
+    double sum = 0.0;
+    for (int i = 0; i < CM; ++i)
+      if (r.live >> i & 1u) sum += exp((double)r.z[i] - x.top);
+    sum = warp_sum(sum);
+    x.sum = sum > 0.0 ? sum : 1.0;
+  }
+  return x;
+}
+
+// The same in 32 bits, with every decision checked.  A key is within err = 2^-19 (softmax) or
+// 2^-21 (sigmoid) + 2^-23 |key| of its 64-bit value: the scores are at most 1; a sigmoid has
+// the errors of an exponential (2^-22 of it, where it moves the score by a quarter at the
+// most), an addition (2^-24) and a reciprocal (2^-23), a softmax those and the 13 roundings
+// of its sum; the bias adds half a step of the key.  Keys more than 2 err apart are in the
+// right order; those that are not, and those only, are compared in 64 bits.  Without a bias
+// the keys are the logits themselves, and exact.  False: too many ties for this way.
+//
+// The k largest are in the k lanes with the largest lane maxima, so they are not below the
+// k-th largest maximum (if that many lanes have an open expert).  What reaches that (some
+// 12 of 256 experts) goes to a lane each, in the order of ids, and finds its place by
+// comparing itself with all the others.
+template <int CM, bool FULL>
+__device__ __forceinline__ bool choose_f32(const Row<CM>& r, const Plan& o, const float* sbias, int lane, int slot0,
+                                           Pool* pool, int* my_e) {
+  const int C = FULL ? CM : o.C;
+  float v[CM];
+  float err = 0.0f;
+  if (o.scores) {
+    float reach = 0.0f;                           // the largest |p + bias|
+    if (o.softmax) {
+      const float top = top_row<CM>(r);
+      float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < CM; ++i) {
-        if constexpr (FAST) biased[i] = (r.live >> i & 1u) ? __fdividef(1.0f, 1.0f + expf(-r.z[i])) : 0.0f;
-        else biased[i] = (r.live >> i & 1u) ? 1.0 / (1.0 + exp(-(double)r.z[i])) : 0.0;
+        v[i] = (r.live >> i & 1u) ? exp_fast(r.z[i] - top) : 0.0f;
+        sum += v[i];
       }
+      sum = warp_sum(sum);
+      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+      for (int i = 0; i < CM; ++i) v[i] *= inv;
+    } else {
+#pragma unroll
+      for (int i = 0; i < CM; ++i) v[i] = rcp_fast(1.0f + exp_fast(-r.z[i]));
     }
     if (o.bias) {
 #pragma unroll
       for (int i = 0; i < CM; ++i)
-        if (r.have >> i & 1u) biased[i] += (F)__ldg(o.bias + lane * C + i);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < CM; ++i) {
-    const F v = o.bias ? biased[i] : (F)r.z[i];
-    key[i] = (r.live >> i & 1u) ? ordered(v) : (r.have >> i & 1u) ? (U)1 : (U)0;
-    if (FAST && scores && (r.live >> i & 1u)) reach = fmaxf(reach, fabsf((float)biased[i]));
-  }
-  bool sure = true;
-  if (FAST && scores) reach = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(reach)));
-
-  if (grouped) {
-    const int S = E / o.n_groups, L = S / C;
-    U mine = 0;                                   // the value of this lane's group, if it speaks for one
-    int shift = 0;                                // group g's speaker is lane g << shift
-    if (S % C == 0 && (L & (L - 1)) == 0) {
-      // groups are aligned runs of L lanes
-      F a = -INFINITY, b = -INFINITY;             // the two largest, a >= b
-#pragma unroll
-      for (int i = 0; i < CM; ++i) {
-        if (r.live >> i & 1u) {
-          const F v = (o.group_top2 || o.bias) ? biased[i] : (F)r.z[i];
-          if (v > a) { b = a; a = v; } else if (v > b) b = v;
-        }
-      }
-      for (int off = 1; off < L; off <<= 1) {
-        const F oa = __shfl_xor_sync(0xffffffffu, a, off), ob = __shfl_xor_sync(0xffffffffu, b, off);
-        b = a >= oa ? (oa > b ? oa : b) : (a > ob ? a : ob);
-        a = a >= oa ? a : oa;
-      }
-      shift = __ffs(L) - 1;
-      const F v = o.group_top2 && b != -INFINITY ? a + b : a;
-      if ((lane & (L - 1)) == 0 && (lane >> shift) < o.n_groups) mine = ordered(v);
-    } else {
-      for (int g = 0; g < o.n_groups; ++g) {
-        F a = -INFINITY, b = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < CM; ++i) {
-          const int e = lane * C + i;
-          if ((r.live >> i & 1u) && e >= g * S && e < g * S + S) {
-            const F v = (o.group_top2 || o.bias) ? biased[i] : (F)r.z[i];
-            if (v > a) { b = a; a = v; } else if (v > b) b = v;
-          }
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-          const F oa = __shfl_xor_sync(0xffffffffu, a, off), ob = __shfl_xor_sync(0xffffffffu, b, off);
-          b = a >= oa ? (oa > b ? oa : b) : (a > ob ? a : ob);
-          a = a >= oa ? a : oa;
-        }
-        const F v = o.group_top2 && b != -INFINITY ? a + b : a;
-        if (lane == g) mine = ordered(v);
-      }
-    }
-    uint32_t chosen = 0;
-    U last = 0;
-    for (int j = 0; j < o.topk_groups; ++j) {
-      last = warp_max(mine);
-      const int who = __ffs(__ballot_sync(0xffffffffu, mine == last)) - 1;
-      chosen |= 1u << (who >> shift);
-      if (lane == who) mine = 0;
-    }
-    if constexpr (FAST) {
-      const uint32_t next = warp_max(mine);
-      if (scores && next > ordered(-INFINITY))
-        sure = unordered(last) - unordered(next) > 7.63e-6f + 9.54e-7f * reach;   // 2^-17, 2^-20: two keys' errors each
+        if (r.live >> i & 1u) v[i] += sbias[lane * C + i];
     }
 #pragma unroll
     for (int i = 0; i < CM; ++i)
-      if (!(chosen >> ((lane * C + i) / S) & 1u)) key[i] = 0;
-  }
-
-  // the lane's best, then the warp's, k times
-  U best = 0;
-  int at = 0;
-  auto rescan = [&] {
-    best = 0;
+      if (r.live >> i & 1u) reach = fmaxf(reach, fabsf(v[i]));
+    reach = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(reach)));
+    err = (o.softmax ? 1.91e-6f : 4.77e-7f) + 1.2e-7f * reach;
+  } else {
 #pragma unroll
-    for (int i = 0; i < CM; ++i)
-      if (key[i] > best) { best = key[i]; at = i; }
-  };
-  rescan();
-  const int rounds = k + (FAST && o.bias ? 1 : 0);
-  U prev = 0;
-  for (int j = 0; j < rounds; ++j) {
-    const U top = warp_max(best);
-    if constexpr (FAST) {
-      if (o.bias && j > 0 && top > 1 && !(unordered(prev) - unordered(top) > 3.815e-6f + 4.77e-7f * reach)) sure = false;
-    }
-    prev = top;
-    if (j == k) break;
-    // lanes hold ascending runs of experts: the lowest lane has the lowest id
-    const int who = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
-    const int e = __shfl_sync(0xffffffffu, lane * C + at, who);
-    if (lane == slot0 + j) *my_e = e;
-    if (lane == who) {
+    for (int i = 0; i < CM; ++i) v[i] = r.z[i];
+  }
+  uint32_t key[CM];
+#pragma unroll
+  for (int i = 0; i < CM; ++i)
+    key[i] = (r.live >> i & 1u) ? ordered(o.bias ? v[i] : r.z[i]) : FULL ? 1u : (r.have >> i & 1u);
+  if (o.grouped) {
+    uint32_t last = 0, next = 0;
+    Two<float> seen = {0.0f, 0.0f};
+    uint32_t chosen = choose_groups(o, lane, group_values<uint32_t>(o, lane, v, r.live, &seen), &last, &next);
+    // a group's value has the errors of two keys and of their sum
+    if (o.scores && next > ordered(-INFINITY) && !(unordered(last) - unordered(next) > 6.0f * err)) {
+      if (!o.L) return false;
+      // in 64 bits: the experts that may be among their group's largest
+      const float least = (o.top2 && seen.b != -INFINITY ? seen.b : seen.a) - 2.0f * err;
+      uint32_t todo = 0;
 #pragma unroll
       for (int i = 0; i < CM; ++i)
-        if (i == at) key[i] = 0;
-      rescan();
+        if ((r.live >> i & 1u) && !(v[i] < least)) todo |= 1u << i;
+      const Exact x = exact_of<CM, FULL>(o.row, o.E, o.softmax, lane);
+      Two<double> t = {-INFINITY, -INFINITY};
+      while (__any_sync(0xffffffffu, todo != 0)) {
+        const int at = __ffs(todo) - 1;
+        todo &= todo - 1;
+        if (at >= 0) t.add(x.score(fminf(__ldg(o.row + lane * C + at), FLT_MAX)) + (o.bias ? (double)sbias[lane * C + at] : 0.0));
+      }
+      __syncwarp();
+      t.join_lanes(o.L);
+      uint64_t last64, next64, mine = 0;
+      if ((lane & (o.L - 1)) == 0 && (lane >> o.shift) < o.n_groups)
+        mine = ordered(o.top2 && t.b != -INFINITY ? t.a + t.b : t.a);
+      chosen = choose_groups(o, lane, mine, &last64, &next64);
+    }
+    close_groups(o, lane, chosen, key);
+  }
+  const int want = o.k + (o.bias ? 1 : 0);        // with a bias the next one too, for its distance
+  uint32_t best = 0, floor = 0;
+#pragma unroll
+  for (int i = 0; i < CM; ++i) best = max(best, key[i]);
+  for (int j = 0; j < want; ++j) {
+    floor = warp_max(best);
+    if (best == floor) best = 0;                  // ties go at once: the floor is only lower for it
+  }
+  // no lanes left: every open expert may be needed; with a bias what is as good as the floor
+  if (o.bias && floor > 1) floor = ordered(unordered(floor) - 2.0f * err);
+  floor = max(floor, 1u);
+  uint32_t in = 0;
+#pragma unroll
+  for (int i = 0; i < CM; ++i) in |= key[i] >= floor ? 1u << i : 0u;
+  // ids ascend from lane to lane: this lane's candidates stand behind the lower lanes'
+  const int mine = __popc(in);
+  const uint32_t below = (1u << lane) - 1u;
+  int at = 0, n = 0;
+#pragma unroll
+  for (int b = 0; (1 << b) <= CM; ++b) {
+    const uint32_t votes = __ballot_sync(0xffffffffu, mine >> b & 1);
+    at += __popc(votes & below) << b;
+    n += __popc(votes) << b;
+  }
+  if (n > 32) return false;
+#pragma unroll
+  for (int i = 0; i < CM; ++i)
+    if (in >> i & 1u) pool->found[at++] = make_uint2(key[i], (uint32_t)(lane * C + i));
+  __syncwarp();
+  const uint2 me = lane < n ? pool->found[lane] : make_uint2(0u, 0u);
+  int rank = 0;
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const uint32_t other = pool->found[j].x;
+    rank += other > me.x || (other == me.x && j < lane);
+  }
+  if (lane < n && rank < want) pool->sorted[rank] = me;
+  __syncwarp();
+  if (o.bias) {
+    bool close = false;
+    if (lane + 1 < min(want, n)) {
+      const uint32_t a = pool->sorted[lane].x, b = pool->sorted[lane + 1].x;
+      close = b > 1 && !(unordered(a) - unordered(b) > 2.0f * err);
+    }
+    if (__any_sync(0xffffffffu, close)) {
+      // in 64 bits: every candidate's key, and its place again
+      const Exact x = exact_of<CM, FULL>(o.row, o.E, o.softmax, lane);
+      uint64_t exact = 0;
+      if (lane < n) exact = me.x == 1 ? 1ull : ordered(x.score(fminf(__ldg(o.row + me.y), FLT_MAX)) + (double)sbias[me.y]);
+      rank = 0;
+      for (int j = 0; j < n; ++j) {
+        const uint64_t other = __shfl_sync(0xffffffffu, exact, j);
+        rank += other > exact || (other == exact && j < lane);
+      }
+      if (lane < n && rank < want) pool->sorted[rank] = me;
+      __syncwarp();
     }
   }
-  return sure;
+  if (lane >= slot0 && lane < slot0 + o.k) *my_e = (int)pool->sorted[lane - slot0].y;
+  __syncwarp();
+  return true;
 }
 
 // A warp routes RS_TOK tokens one after the other; then lane 8 q + j makes the gate of
 // token q's slot j in 64 bits, one exponential for all of them.
-template <int CM>
-__global__ void __launch_bounds__(RS_WARPS * 32)
+template <int CM, bool FULL>
+__global__ void __launch_bounds__(RS_WARPS * 32, 4)
 route_scored_kernel(const float* __restrict__ logits, int T, int E, int k, const RouterArgs o,
                     int32_t* __restrict__ topk_idx, float* __restrict__ topk_gate,
                     int32_t* __restrict__ blk_hist, uint32_t* __restrict__ arrive,
@@ -258,25 +459,31 @@ route_scored_kernel(const float* __restrict__ logits, int T, int E, int k, const
   pdl_trigger();
   pdl_wait();
   __shared__ int hist[MAX_E];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, C = cdiv(E, 32);
-  if (blk_hist) {
-    for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, C = FULL ? CM : cdiv(E, 32);
+  __shared__ __align__(16) float sbias[MAX_E];
+  if (blk_hist || o.bias) {
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+      hist[e] = 0;
+      if (o.bias) sbias[e] = __ldg(o.bias + e);
+    }
     __syncthreads();
   }
+  __shared__ Pool pools[RS_WARPS];
+  Pool* pool = &pools[warp];
+  Plan plan = plan_of(E, k, o);
   const int t0 = blockIdx.x * ROUTE_TOK + warp;   // its tokens: t0, t0 + 8, ..
   int my_e = 0;
   float my_top = 0.0f, my_sum = 1.0f;
-  Row<CM> next;
-  if (t0 < T) load_row<CM>(logits + (size_t)t0 * E, E, C, lane, next);
 #pragma unroll 1
   for (int q = 0; q < RS_TOK; ++q) {
     const int t = t0 + q * RS_WARPS;
     if (t >= T) break;
-    Row<CM> r = next;
-    if (q + 1 < RS_TOK && t + RS_WARPS < T) load_row<CM>(logits + (size_t)(t + RS_WARPS) * E, E, C, lane, next);
-    mask_row<CM>(E, C, lane, r);
-    if (!choose<float, uint32_t, CM>(r, E, C, k, o, lane, q * MAX_K, &my_e))
-      choose<double, uint64_t, CM>(r, E, C, k, o, lane, q * MAX_K, &my_e);
+    Row<CM> r;
+    load_row<CM, FULL>(logits + (size_t)t * E, E, C, lane, r);
+    mask_row<CM, FULL>(E, C, lane, r);
+    plan.row = logits + (size_t)t * E;
+    if (!choose_f32<CM, FULL>(r, plan, sbias, lane, q * MAX_K, pool, &my_e))
+      my_e = choose_f64<CM, FULL>(plan, lane, q * MAX_K, my_e);
     if (o.score == 0) {
       float ex[CM], top, sum = 1.0f;
       if (o.renorm) top = top_row<CM>(r);         // the sum cancels
@@ -315,15 +522,16 @@ route_scored_kernel(const float* __restrict__ logits, int T, int E, int k, const
 //   softmax: dz_e = p_e (dp_e - sum_j p_j dp_j);  sigmoid: dz_e = dp_e p_e (1 - p_e).
 // With renorm the softmax's own normaliser cancels, and dz is 0 beside the chosen.
 // A warp takes 4 tokens: lane 8 q + j is token q's slot j, in 64 bits; then the warp
-// writes the 4 rows.  `zero`: nothing but the chosen experts' own gradients.
-template <int CM>
+// writes the 4 rows, and the slots their experts' values over them.  `zero`: there is
+// nothing beside the chosen.
+template <int CM, bool FULL>
 __global__ void __launch_bounds__(256)
 route_scored_bwd_kernel(const float* __restrict__ dgate, const float* __restrict__ logits,
                         const int32_t* __restrict__ topk_idx, int T, int E, int k, const RouterArgs o,
                         float* __restrict__ dlogits) {
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31, j = lane & 7, C = cdiv(E, 32);
+  const int lane = threadIdx.x & 31, j = lane & 7, C = FULL ? CM : cdiv(E, 32);
   const int t0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * 4;
   if (t0 >= T) return;
   const int t = t0 + (lane >> 3);
@@ -340,8 +548,8 @@ route_scored_bwd_kernel(const float* __restrict__ dgate, const float* __restrict
 #pragma unroll 1
     for (int q = 0; q < 4 && t0 + q < T; ++q) {
       Row<CM> r;
-      load_row<CM>(logits + (size_t)(t0 + q) * E, E, C, lane, r);
-      mask_row<CM>(E, C, lane, r);
+      load_row<CM, FULL>(logits + (size_t)(t0 + q) * E, E, C, lane, r);
+      mask_row<CM, FULL>(E, C, lane, r);
       float ex[CM], top, sum;
       softmax_row<CM>(r, ex, &top, &sum);
       if (lane >> 3 == q) { my_top = top; my_sum = sum > 0.0f ? sum : 1.0f; }
@@ -363,58 +571,68 @@ route_scored_bwd_kernel(const float* __restrict__ dgate, const float* __restrict
   }
   const double dot = zero ? 0.0 : sum8(w * dp);
   const float dz = live ? (float)(o.score == 0 ? w * (dp - dot) : dp * w * (1.0 - w)) : 0.0f;
+  if (zero) {
+    // 4 rows of zeros in one run
+    const int rows = min(4, T - t0), n = rows * E;
+    float* out = dlogits + (size_t)t0 * E;
+    if ((E & 3) == 0) {
+      for (int i = lane * 4; i < n; i += 128) *reinterpret_cast<float4*>(out + i) = make_float4(0, 0, 0, 0);
+    } else {
+      for (int i = lane; i < n; i += 32) out[i] = 0.0f;
+    }
+  } else {
 #pragma unroll 1
-  for (int q = 0; q < 4 && t0 + q < T; ++q) {
-    float v[CM] = {};
-    if (!zero) {
+    for (int q = 0; q < 4 && t0 + q < T; ++q) {
+      float v[CM] = {};
       const float top = __shfl_sync(0xffffffffu, my_top, q * 8);
       const float by = (float)-__shfl_sync(0xffffffffu, dot / (double)my_sum, q * 8);
       Row<CM> r;
-      load_row<CM>(logits + (size_t)(t0 + q) * E, E, C, lane, r);
-      mask_row<CM>(E, C, lane, r);
+      load_row<CM, FULL>(logits + (size_t)(t0 + q) * E, E, C, lane, r);
+      mask_row<CM, FULL>(E, C, lane, r);
 #pragma unroll
       for (int i = 0; i < CM; ++i)
         if (r.live >> i & 1u) v[i] = expf(r.z[i] - top) * by;
-    }
-    for (int s = 0; s < k; ++s) {
-      const int es = __shfl_sync(0xffffffffu, e, q * 8 + s);
-      const float ds = __shfl_sync(0xffffffffu, dz, q * 8 + s);
-      const int at = es - lane * C;
+      float* out = dlogits + (size_t)(t0 + q) * E + lane * C;
+      if (CM >= 4 && C == CM && (E & 3) == 0) {
 #pragma unroll
-      for (int i = 0; i < CM; ++i)
-        if (i < C && es >= 0 && at == i) v[i] = ds;
-    }
-    float* out = dlogits + (size_t)(t0 + q) * E + lane * C;
-    if (CM >= 4 && C == CM && (E & 3) == 0) {
+        for (int i = 0; i < CM / 4; ++i)
+          if (lane * C + 4 * i < E)
+            reinterpret_cast<float4*>(out)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      } else {
 #pragma unroll
-      for (int i = 0; i < CM / 4; ++i)
-        if (lane * C + 4 * i < E)
-          reinterpret_cast<float4*>(out)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < CM; ++i)
-        if (i < C && lane * C + i < E) out[i] = v[i];
+        for (int i = 0; i < CM; ++i)
+          if (i < C && lane * C + i < E) out[i] = v[i];
+      }
     }
   }
+  __syncwarp();                                   // the chosen experts' own values come after
+  if (e >= 0) dlogits[(size_t)t * E + e] = dz;
 }
 
 }  // namespace
 
+template <template <int, bool> class K, typename... Args>
+cudaError_t launch_rows(int E, int grid, cudaStream_t s, Args... args) {
+  const bool full = E == 32 || E == 64 || E == 128 || E == 256;
+  auto kernel = E <= 32 ? (full ? K<1, true>::at : K<1, false>::at)
+                : E <= 64 ? (full ? K<2, true>::at : K<2, false>::at)
+                : E <= 128 ? (full ? K<4, true>::at : K<4, false>::at)
+                           : (full ? K<8, true>::at : K<8, false>::at);
+  return launch_pdl(kernel, dim3((unsigned)grid), dim3(256), 0, s, args...);
+}
+template <int CM, bool FULL> struct Forward { static constexpr auto at = route_scored_kernel<CM, FULL>; };
+template <int CM, bool FULL> struct Backward { static constexpr auto at = route_scored_bwd_kernel<CM, FULL>; };
+
 cudaError_t launch_route_scored(const float* logits, int T, int E, int k, const RouterArgs& r,
                                 int32_t* topk_idx, float* topk_gate, int32_t* blk_hist,
                                 uint32_t* arrive, uint32_t* ready_q, cudaStream_t s) {
-  auto kernel = E <= 32 ? route_scored_kernel<1> : E <= 64 ? route_scored_kernel<2>
-                : E <= 128 ? route_scored_kernel<4> : route_scored_kernel<8>;
-  return launch_pdl(kernel, dim3(route_blocks(T)), dim3(RS_WARPS * 32), 0, s, logits, T, E, k, r, topk_idx, topk_gate,
-                    blk_hist, arrive, ready_q);
+  return launch_rows<Forward>(E, route_blocks(T), s, logits, T, E, k, r, topk_idx, topk_gate, blk_hist, arrive, ready_q);
 }
 
 cudaError_t launch_route_scored_bwd(const float* dgate, const float* logits, const int32_t* topk_idx,
                                     int T, int E, int k, const RouterArgs& r, float* dlogits,
                                     cudaStream_t s) {
-  auto kernel = E <= 32 ? route_scored_bwd_kernel<1> : E <= 64 ? route_scored_bwd_kernel<2>
-                : E <= 128 ? route_scored_bwd_kernel<4> : route_scored_bwd_kernel<8>;
-  return launch_pdl(kernel, dim3(cdiv(T, 32)), dim3(256), 0, s, dgate, logits, topk_idx, T, E, k, r, dlogits);
+  return launch_rows<Backward>(E, cdiv(T, 32), s, dgate, logits, topk_idx, T, E, k, r, dlogits);
 }
 
 }  // namespace moe
