@@ -908,15 +908,19 @@ Shape pick(const GemmProblem& p, int dev, int nsm) {
   const int nkb = cdiv(p.K, 64), most = min(p.B.planes > 1 ? 128 : 256, cdiv(p.N, 32) * 32);
   const int slices = p.ws ? gemm_slices(p.M, p.N) : 1;
   for (int CG = 1; CG <= (p.M > 128 ? 2 : 1); ++CG) {
-    for (int BN = CG == 1 && p.N <= 16 ? 16 : 32; BN <= most; BN += 32) {
-      const int tiles = cdiv(p.M, 128 * CG) * cdiv(p.N, BN), fit = clusters_of(dev, nsm, CG);
+    const int rows = cdiv(p.M, 128 * CG), fit = clusters_of(dev, nsm, CG);
+    for (int BN = CG == 1 && p.N <= 16 ? 16 : 32, before = 0; BN <= most; BN += 32) {
+      const int cols = cdiv(p.N, BN);
+      if (cols == before && BN % 128 != 0) continue;   // wider for no fewer tiles
+      before = cols;
+      const int tiles = rows * cols;
       consider({CG, BN, 1, 1});
       for (int S = 2; S * CG <= 8; S *= 2) {
-        if (tiles > clusters_of(dev, nsm, S * CG) || nkb < 4 * S) break;
+        if (nkb < 4 * S || tiles > clusters_of(dev, nsm, S * CG)) break;
         consider({CG, BN, S, 1});
       }
       // slices that fill one wave of CTAs, or two
-      for (int w = 1; w <= 2; ++w) {
+      for (int w = 1; w <= 2 && slices > 1; ++w) {
         const int SW = min(min(slices, fit * w / tiles), nkb / 4);
         if (SW > 1) consider({CG, BN, 1, SW});
       }

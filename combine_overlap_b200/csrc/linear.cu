@@ -73,26 +73,12 @@ size_t pack_bytes(long rows, int n) { return n % 8 ? up256((size_t)rows * pad8(n
 // stand side by side in a row of its own: term 0 = bf16(du), term p = bf16(du - the
 // earlier terms), n8 columns each.  `part`
 // [gridDim.y][N] (optional): the block's column sums, in a fixed order.
-// What bounds it is memory: R rows' loads are in flight per thread.
+// Memory bounds it: the loads of DACT_R rows are issued before the first is used.  MODE: dout
+// in bf16 or fp32 with rows of 16-byte multiples, or any (element by element).
 constexpr int DACT_R = 4;
+enum { DACT_BF16, DACT_F32, DACT_ANY };
 
-__device__ __forceinline__ void dact_load(const void* __restrict__ dout, int f32, size_t at, int n, int N, bool vec,
-                                          float (&v)[8]) {
-  if (!vec) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      v[i] = n + i >= N ? 0.0f : f32 ? static_cast<const float*>(dout)[at + i]
-                                     : __bfloat162float(static_cast<const __nv_bfloat16*>(dout)[at + i]);
-  } else if (f32) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(dout) + at));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(dout) + at) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(dout) + at)), v);
-  }
-}
-
-template <int ACT>
+template <int ACT, int MODE>
 __global__ void __launch_bounds__(256) dact_kernel(const void* __restrict__ dout, int f32,
                                                    const __nv_bfloat16* __restrict__ pre, int M,
                                                    int N, int rows, int planes, __nv_bfloat16* __restrict__ du,
@@ -101,18 +87,43 @@ __global__ void __launch_bounds__(256) dact_kernel(const void* __restrict__ dout
   pdl_wait();
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int n = blockIdx.x * 128 + tx * 8;
-  const bool vec = (N & 7) == 0;
   const int m1 = min(M, (int)(blockIdx.y + 1) * rows);
   float sum[8] = {};
   if (n < n8) {
     for (int m0 = blockIdx.y * rows + ty; m0 < m1; m0 += 16 * DACT_R) {
-      float v[DACT_R][8], u[ACT ? DACT_R : 1][8];
+      float v[DACT_R][8], u[DACT_R][8];
+      if constexpr (MODE == DACT_ANY) {
 #pragma unroll
-      for (int r = 0; r < DACT_R; ++r) {
-        const int m = m0 + 16 * r;
-        if (m < m1) {
-          dact_load(dout, f32, (size_t)m * N + n, n, N, vec, v[r]);
-          if (ACT) dact_load(pre, 0, (size_t)m * N + n, n, N, vec, u[ACT ? r : 0]);
+        for (int r = 0; r < DACT_R; ++r) {
+          const size_t at = (size_t)min(m0 + 16 * r, m1 - 1) * N + n;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            v[r][i] = n + i >= N ? 0.0f : f32 ? static_cast<const float*>(dout)[at + i]
+                                              : __bfloat162float(static_cast<const __nv_bfloat16*>(dout)[at + i]);
+            if (ACT) u[r][i] = n + i >= N ? 0.0f : __bfloat162float(pre[at + i]);
+          }
+        }
+      } else {
+        uint4 d[DACT_R][MODE == DACT_F32 ? 2 : 1], x[DACT_R];
+#pragma unroll
+        for (int r = 0; r < DACT_R; ++r) {
+          const size_t at = (size_t)min(m0 + 16 * r, m1 - 1) * N + n;
+          const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(dout) + at * (MODE == DACT_F32 ? 4 : 2));
+          d[r][0] = __ldg(q);
+          if (MODE == DACT_F32) d[r][MODE == DACT_F32 ? 1 : 0] = __ldg(q + 1);
+          if (ACT) x[r] = __ldg(reinterpret_cast<const uint4*>(pre + at));
+        }
+#pragma unroll
+        for (int r = 0; r < DACT_R; ++r) {
+          if constexpr (MODE == DACT_F32) {
+            v[r][0] = __uint_as_float(d[r][0].x); v[r][1] = __uint_as_float(d[r][0].y);
+            v[r][2] = __uint_as_float(d[r][0].z); v[r][3] = __uint_as_float(d[r][0].w);
+            v[r][4] = __uint_as_float(d[r][1].x); v[r][5] = __uint_as_float(d[r][1].y);
+            v[r][6] = __uint_as_float(d[r][1].z); v[r][7] = __uint_as_float(d[r][1].w);
+          } else {
+            bf16x8_to_f32(d[r][0], v[r]);
+          }
+          if (ACT) bf16x8_to_f32(x[r], u[r]);
         }
       }
 #pragma unroll
@@ -121,14 +132,15 @@ __global__ void __launch_bounds__(256) dact_kernel(const void* __restrict__ dout
         if (m >= m1) break;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if (ACT) v[r][i] *= dact_f32(ACT, u[ACT ? r : 0][i]);
+          if (ACT) v[r][i] *= dact_f32(ACT, u[r][i]);
           sum[i] += v[r][i];
         }
-        for (int p = 0; p < planes; ++p) {
+        __nv_bfloat16* to = du + (size_t)m * planes * n8 + n;
+        for (int p = 0; p < planes; ++p, to += n8) {
           uint32_t w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(v[r][2 * i], v[r][2 * i + 1]);
-          *reinterpret_cast<uint4*>(du + ((size_t)m * planes + p) * n8 + n) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
           if (p + 1 == planes) break;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -152,6 +164,14 @@ __global__ void __launch_bounds__(256) dact_kernel(const void* __restrict__ dout
     for (int r = 0; r < 16; ++r) s += sh[r][c];
     part[(size_t)blockIdx.y * N + blockIdx.x * 128 + c] = s;
   }
+}
+
+template <int ACT>
+cudaError_t launch_dact(const LinearBwdArgs& a, int rows, int planes, __nv_bfloat16* du, int n8, float* part,
+                        cudaStream_t s) {
+  auto kernel = a.N % 8 ? dact_kernel<ACT, DACT_ANY> : a.dout_f32 ? dact_kernel<ACT, DACT_F32> : dact_kernel<ACT, DACT_BF16>;
+  return launch_pdl(kernel, dim3(cdiv(n8, 128), cdiv(a.M, rows)), dim3(256), 0, s, a.dout, a.dout_f32,
+                    static_cast<const __nv_bfloat16*>(a.pre), a.M, a.N, rows, planes, du, n8, part);
 }
 
 // 32 columns per block, 8 warps each a run of the blocks' sums.
@@ -238,11 +258,11 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, void* ws, cudaStream_t s) 
   // dout is an operand as it stands if it is bf16, unpadded and without an activation
   const bool direct = !a.dout_f32 && !a.act && n8 == a.N;
   if (!direct || a.dbias) {
-    auto kernel = a.act == 1 ? dact_kernel<1> : a.act == 2 ? dact_kernel<2> : a.act == 3 ? dact_kernel<3> : dact_kernel<0>;
-    cudaError_t e = launch_pdl(kernel, dim3(cdiv(n8, 128), nblk), dim3(256), 0, s, a.dout, a.dout_f32,
-                               static_cast<const __nv_bfloat16*>(a.pre), a.M, a.N, rows,
-                               direct ? 0 : t.n, (__nv_bfloat16*)du.p, n8,
-                               a.dbias ? part : nullptr);
+    float* sums = a.dbias ? part : nullptr;
+    __nv_bfloat16* to = (__nv_bfloat16*)du.p;
+    const int n = direct ? 0 : t.n;
+    cudaError_t e = a.act == 1 ? launch_dact<1>(a, rows, n, to, n8, sums, s) : a.act == 2 ? launch_dact<2>(a, rows, n, to, n8, sums, s)
+                    : a.act == 3 ? launch_dact<3>(a, rows, n, to, n8, sums, s) : launch_dact<0>(a, rows, n, to, n8, sums, s);
     if (e != cudaSuccess) return e;
   }
   if (direct) du = {a.dout, (size_t)n8 * 2, 0, 1};
