@@ -462,12 +462,13 @@ assert (_LINEAR.size, _LINEAR_BWD.size, _ROUTER.size) == tuple(
 _BF16, _F32 = torch.bfloat16, torch.float32
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = torch.cuda.current_device
 
 
 def _same_device(*named):
     """Every given tensor on one device, the current one: the library launches there.
     Returns its current stream."""
-    cur = torch.cuda.current_device()
+    cur = _current_device()
     for t, name in named:
         if t is not None and t.get_device() != cur:
             raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{cur}")
@@ -484,20 +485,26 @@ def _dtype_code(dtype, name: str) -> int:
 
 def _need2(t, dtype, name: str):
     """The shape of a contiguous 2-D CUDA tensor of dtype."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous():
-        shape = t.shape
-        if len(shape) == 2:
-            return shape
+    try:
+        if t.dtype is dtype and t.is_cuda and t.is_contiguous():
+            shape = t.shape
+            if len(shape) == 2:
+                return shape
+    except AttributeError:
+        pass
     _need(t, dtype, name)
     raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
 
 
 def _given(t, dtype, shape: tuple, name: str) -> int:
     """The address of a contiguous CUDA tensor of dtype and shape."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous()):
-        _need(t, dtype, name)
-    if t.shape != shape:
-        _shape(t, shape, name)
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, dtype, name)
+    _shape(t, shape, name)
     return t.data_ptr()
 
 
@@ -531,21 +538,24 @@ def linear(x, W, bias=None, residual=None, act=ACT_NONE, out_dtype=torch.bfloat1
         with torch.cuda.stream(stream):
             return linear(x, W, bias, residual, act, out_dtype, pre, out, ws)
     M, K = _need2(x, _BF16, "x")
-    N = _need2(W, _BF16, "W")[1]
-    w_ptr = _given(W, _BF16, (K, N), "W")
+    Kw, N = _need2(W, _BF16, "W")
+    if Kw != K:
+        _shape(W, (K, N), "W")
     code = _dtype_code(out_dtype, "out_dtype")
     b_ptr = _given(bias, _F32, (N,), "bias") if bias is not None else 0
     r_ptr = _given(residual, out_dtype, (M, N), "residual") if residual is not None else 0
-    if out is None:
-        out = x.new_empty((M, N), dtype=out_dtype)
-    else:
+    if out is not None:
         _given(out, out_dtype, (M, N), "out")
+    elif residual is not None:
+        out = torch.empty_like(residual)
+    else:
+        out = x.new_empty((M, N), dtype=out_dtype)
     u = x.new_empty((M, N)) if pre else None
     ws = _scratch(ws, _lib.moe_linear_workspace_size(M, K, N), x, "moe_linear_workspace_size")
     st = _same_device((x, "x"), (W, "W"), (bias, "bias"), (residual, "residual"), (out, "out"), (ws, "ws"))
-    a = _LINEAR.pack(M, K, N, x.data_ptr(), w_ptr, b_ptr, r_ptr, act, code, out.data_ptr(),
+    a = _LINEAR.pack(M, K, N, x.data_ptr(), W.data_ptr(), b_ptr, r_ptr, act, code, out.data_ptr(),
                      u.data_ptr() if pre else 0)
-    r = _lib.moe_linear(a, *((None, 0) if ws is None else (ws.data_ptr(), ws.numel())), st)
+    r = _lib.moe_linear(a, None, 0, st) if ws is None else _lib.moe_linear(a, ws.data_ptr(), ws.numel(), st)
     if r:
         _check(r, "moe_linear")
     return (out, u) if pre else out
@@ -561,8 +571,9 @@ def linear_backward(dout, x, W, pre=None, act=ACT_NONE, dW_dtype=torch.float32, 
         with torch.cuda.stream(stream):
             return linear_backward(dout, x, W, pre, act, dW_dtype, want_dx, want_dW, want_dbias, ws)
     M, K = _need2(x, _BF16, "x")
-    N = _need2(W, _BF16, "W")[1]
-    w_ptr = _given(W, _BF16, (K, N), "W")
+    Kw, N = _need2(W, _BF16, "W")
+    if Kw != K:
+        _shape(W, (K, N), "W")
     code, dW_code = _dtype_code(dout.dtype, "dout"), _dtype_code(dW_dtype, "dW_dtype")
     d_ptr = _given(dout, dout.dtype, (M, N), "dout")
     p_ptr = 0
@@ -572,12 +583,12 @@ def linear_backward(dout, x, W, pre=None, act=ACT_NONE, dW_dtype=torch.float32, 
         p_ptr = _given(pre, _BF16, (M, N), "pre")
     else:
         pre = None
-    dx = x.new_empty((M, K)) if want_dx else None
-    dW = x.new_empty((K, N), dtype=dW_dtype) if want_dW else None
+    dx = torch.empty_like(x) if want_dx else None
+    dW = torch.empty_like(W, dtype=dW_dtype) if want_dW else None
     db = x.new_empty(N, dtype=_F32) if want_dbias else None
     ws = _scratch(ws, _lib.moe_linear_backward_workspace_size(M, K, N), x, "moe_linear_backward_workspace_size")
     st = _same_device((x, "x"), (W, "W"), (dout, "dout"), (pre, "pre"), (ws, "ws"))
-    a = _LINEAR_BWD.pack(M, K, N, d_ptr, x.data_ptr(), w_ptr, p_ptr, act, code, dW_code,
+    a = _LINEAR_BWD.pack(M, K, N, d_ptr, x.data_ptr(), W.data_ptr(), p_ptr, act, code, dW_code,
                          dx.data_ptr() if want_dx else 0, dW.data_ptr() if want_dW else 0,
                          db.data_ptr() if want_dbias else 0)
     r = _lib.moe_linear_backward(a, *((None, 0) if ws is None else (ws.data_ptr(), ws.numel())), st)
@@ -637,7 +648,7 @@ def route_scored_backward(dgate, logits, topk_idx, score=SCORE_SOFTMAX, renorm=T
     d_ptr = _given(dgate, _F32, (T, k), "dgate")
     i_ptr = _given(topk_idx, torch.int32, (T, k), "topk_idx")
     if dlogits is None:
-        dlogits = logits.new_empty((T, E))
+        dlogits = torch.empty_like(logits)
     else:
         _given(dlogits, _F32, (T, E), "dlogits")
     st = _same_device((logits, "logits"), (dgate, "dgate"), (topk_idx, "topk_idx"), (dlogits, "dlogits"))
@@ -664,8 +675,8 @@ def combine_backward(dout, y, row_of, topk_gate, want_dy=True, dy=None, stream=N
     if dy is not None:
         _given(dy, _BF16, (T * k, d), "dy")
     elif want_dy:
-        dy = y.new_empty((T * k, d))
-    dgate = topk_gate.new_empty((T, k))
+        dy = torch.empty_like(y)
+    dgate = torch.empty_like(topk_gate)
     st = _same_device((dout, "dout"), (y, "y"), (row_of, "row_of"), (topk_gate, "topk_gate"), (dy, "dy"))
     r = _lib.moe_combine_backward(o_ptr, y_ptr, r_ptr, topk_gate.data_ptr(), T, d, k,
                                   None if dy is None else dy.data_ptr(), dgate.data_ptr(), st)
