@@ -207,6 +207,7 @@ inline bool ok_dtype(int t) { return t == MOE_DTYPE_BF16 || t == MOE_DTYPE_F32; 
 moe_status check_linear_shape(int M, int K, int N) {
   if (M < 1 || K < 1 || N < 1) return MOE_ERR_INVALID;
   const long long lim = 1LL << 40;
+  if (M > 1 << 30 || K > 1 << 30 || N > 1 << 30) return MOE_ERR_UNSUPPORTED;
   if ((long long)M * K >= lim || (long long)K * N >= lim || (long long)M * N >= lim) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

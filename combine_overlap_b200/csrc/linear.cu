@@ -29,41 +29,52 @@ inline int pad8(int n) { return cdiv(n, 8) * 8; }
 inline size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 // ------------------------------------------------------------------- pack ---
-// [rows][n] -> [rows][n8], the pad zero: one thread per 8 output columns.
-__global__ void __launch_bounds__(256) pack_kernel(const __nv_bfloat16* __restrict__ in, long rows, int n,
-                                                   int n8, uint4* __restrict__ out) {
+// Up to two matrices [rows][n] -> [rows][n8], the pad zero: one thread per 8 output columns.
+struct PackJob {
+  const unsigned short* in;
+  uint4* out;
+  long rows;
+  int n;                                  // 0: no such job
+};
+
+__global__ void __launch_bounds__(256) pack_kernel(const PackJob a, const PackJob b) {
   pdl_trigger();
   pdl_wait();
-  const long per = n8 / 8, total = rows * per;
+  const long first = a.rows * cdiv(a.n, 8), total = first + b.rows * cdiv(b.n, 8);
   for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long)gridDim.x * 256) {
-    const long r = i / per;
-    const int c = (int)(i - r * per) * 8;
-    const unsigned short* src = reinterpret_cast<const unsigned short*>(in) + r * n + c;
+    const bool second = i >= first;
+    const long at = second ? i - first : i;
+    const int n = second ? b.n : a.n, per = cdiv(n, 8);
+    const long r = at / per;
+    const int c = (int)(at - r * per) * 8;
+    const unsigned short* src = (second ? b.in : a.in) + r * n + c;
     uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t lo = c + 2 * j < n ? src[2 * j] : 0u, hi = c + 2 * j + 1 < n ? src[2 * j + 1] : 0u;
       w[j] = lo | hi << 16;
     }
-    out[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    (second ? b.out : a.out)[at] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
-// `in` as an operand: itself, or its padded copy at `at` (advanced past it).
-cudaError_t pack(const void* in, long rows, int n, char** at, GemmOperand* o, cudaStream_t s) {
+// `in` [rows][n] as an operand: itself, or its padded copy at `at` (advanced past it), which
+// *job makes.
+GemmOperand operand(const void* in, long rows, int n, char** at, PackJob* job) {
   const int n8 = pad8(n);
-  o->ld = (size_t)n8 * 2;
-  o->plane = 0;
-  o->planes = 1;
-  o->p = in;
-  if (n8 == n) return cudaSuccess;
-  o->p = *at;
-  uint4* out = reinterpret_cast<uint4*>(*at);
+  GemmOperand o = {in, (size_t)n8 * 2, 0, 1};
+  if (n8 == n || !in) return o;
+  o.p = *at;
+  *job = {static_cast<const unsigned short*>(in), reinterpret_cast<uint4*>(*at), rows, n};
   *at += up256((size_t)rows * n8 * 2);
-  const long total = rows * (n8 / 8);
+  return o;
+}
+
+cudaError_t pack(const PackJob& a, const PackJob& b, cudaStream_t s) {
+  const long total = a.rows * cdiv(a.n, 8) + b.rows * cdiv(b.n, 8);
+  if (total == 0) return cudaSuccess;
   const int grid = (int)(total + 255 < 148L * 16 * 256 ? (total + 255) / 256 : 148L * 16);
-  return launch_pdl(pack_kernel, dim3(grid), dim3(256), 0, s, static_cast<const __nv_bfloat16*>(in), rows, n,
-                    n8, out);
+  return launch_pdl(pack_kernel, dim3(grid), dim3(256), 0, s, a, b);
 }
 
 size_t pack_bytes(long rows, int n) { return n % 8 ? up256((size_t)rows * pad8(n) * 2) : 0; }
@@ -208,22 +219,22 @@ int dact_rows(int M, int N) {
 // The bf16 terms that du goes in as.  bf16 gradients take it rounded once, as a stored
 // bf16 gradient would be: an error of the size of their own rounding.  An fp32 dW takes
 // three terms, all 24 bits.  dout in bf16 without an activation is du itself.
-struct Terms { int dx, dW, n; };
-Terms terms_of(const LinearBwdArgs& a) {
-  Terms t;
-  const bool exact = !a.dout_f32 && !a.act;
-  t.dx = a.dx ? 1 : 0;
-  t.dW = a.dW ? (!exact && a.dW_f32 ? 3 : 1) : 0;
-  t.n = max(t.dx, t.dW);
-  return t;
-}
+int terms_of(const LinearBwdArgs& a) { return (a.dout_f32 || a.act) && a.dW && a.dW_f32 ? 3 : 1; }
 
 }  // namespace
 
-// Up to SMALL_M rows go without the tensor cores (linear_small.cu).
-constexpr int SMALL_M = 8;
+// Without the tensor cores (linear_small.cu) where that measured faster, launch included.
+// Rows as they are: 3.4 against 4.5 us at 1 x 2048 x 64, 7.2 against 7.5 at 4 x 2048 x 1024;
+// the tensor cores' stream is ahead from 8 x 2048 x 64 (5.8 / 4.7) and 1 x 4096 x 4096
+// (13.2 / 12.7).  Where they need padded copies first (a launch and a workspace): 9 against
+// 15 us at 4 x 2048 x 1023, 16 against 15 at 16 x 2048 x 1023, 25 against 26 at
+// 1 x 4096 x 4095, 37 against 26 at 8.
+bool is_small(int M, int K, int N) {
+  if (K % 8 == 0 && N % 8 == 0) return M <= 4 && (long long)K * N <= 1LL << 22;
+  return M <= 16 && (long long)M * K * N <= 1LL << 25;
+}
 
-size_t linear_ws_bytes(int M, int K, int N) { return M <= SMALL_M ? 0 : pack_bytes(M, K) + pack_bytes(K, N); }
+size_t linear_ws_bytes(int M, int K, int N) { return is_small(M, K, N) ? 0 : pack_bytes(M, K) + pack_bytes(K, N); }
 
 size_t linear_bwd_ws_bytes(int M, int K, int N) {
   return up256((size_t)cdiv(M, dact_rows(M, N)) * N * 4) + 3 * up256((size_t)M * pad8(N) * 2) + pack_bytes(M, K) +
@@ -231,15 +242,17 @@ size_t linear_bwd_ws_bytes(int M, int K, int N) {
 }
 
 cudaError_t launch_linear(const LinearArgs& a, void* ws, cudaStream_t s) {
-  if (a.M <= SMALL_M) {
+  if (is_small(a.M, a.K, a.N)) {
     int nsm = 0;
     const cudaError_t e = device_of(nullptr, &nsm);
     return e == cudaSuccess ? launch_linear_small(a, nsm, s) : e;
   }
   char* at = static_cast<char*>(ws);
   GemmProblem p = {};
-  cudaError_t e = pack(a.x, a.M, a.K, &at, &p.A, s);
-  if (e == cudaSuccess) e = pack(a.W, a.K, a.N, &at, &p.B, s);
+  PackJob jx = {}, jw = {};
+  p.A = operand(a.x, a.M, a.K, &at, &jx);
+  p.B = operand(a.W, a.K, a.N, &at, &jw);
+  const cudaError_t e = pack(jx, jw, s);
   if (e != cudaSuccess) return e;
   p.b_mn = 1;
   p.M = a.M; p.N = a.N; p.K = a.K;
@@ -252,31 +265,34 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, void* ws, cudaStream_t s) 
   const int rows = dact_rows(a.M, a.N), nblk = cdiv(a.M, rows), n8 = pad8(a.N);
   float* part = reinterpret_cast<float*>(at);
   at += up256((size_t)nblk * a.N * 4);
-  const Terms t = terms_of(a);
-  GemmOperand du = {at, (size_t)t.n * n8 * 2, (size_t)n8 * 2, t.n};
+  const int terms = terms_of(a);
+  GemmOperand du = {at, (size_t)terms * n8 * 2, (size_t)n8 * 2, terms};
   at += 3 * up256((size_t)a.M * n8 * 2);
+  PackJob jx = {}, jw = {};
+  const GemmOperand x = operand(a.dW ? a.x : nullptr, a.M, a.K, &at, &jx);
+  const GemmOperand W = operand(a.dx ? a.W : nullptr, a.K, a.N, &at, &jw);
+  cudaError_t e = pack(jx, jw, s);
+  if (e != cudaSuccess) return e;
   // dout is an operand as it stands if it is bf16, unpadded and without an activation
   const bool direct = !a.dout_f32 && !a.act && n8 == a.N;
   if (!direct || a.dbias) {
-    float* sums = a.dbias ? part : nullptr;
+    float* sums = !a.dbias ? nullptr : nblk == 1 ? a.dbias : part;
     __nv_bfloat16* to = (__nv_bfloat16*)du.p;
-    const int n = direct ? 0 : t.n;
-    cudaError_t e = a.act == 1 ? launch_dact<1>(a, rows, n, to, n8, sums, s) : a.act == 2 ? launch_dact<2>(a, rows, n, to, n8, sums, s)
-                    : a.act == 3 ? launch_dact<3>(a, rows, n, to, n8, sums, s) : launch_dact<0>(a, rows, n, to, n8, sums, s);
+    const int n = direct ? 0 : terms;
+    e = a.act == 1 ? launch_dact<1>(a, rows, n, to, n8, sums, s) : a.act == 2 ? launch_dact<2>(a, rows, n, to, n8, sums, s)
+        : a.act == 3 ? launch_dact<3>(a, rows, n, to, n8, sums, s) : launch_dact<0>(a, rows, n, to, n8, sums, s);
     if (e != cudaSuccess) return e;
   }
   if (direct) du = {a.dout, (size_t)n8 * 2, 0, 1};
-  if (a.dbias) {
-    cudaError_t e = launch_pdl(dbias_kernel, dim3(cdiv(a.N, 32)), dim3(256), 0, s, (const float*)part, nblk,
-                               a.N, a.dbias);
+  if (a.dbias && nblk > 1) {
+    e = launch_pdl(dbias_kernel, dim3(cdiv(a.N, 32)), dim3(256), 0, s, (const float*)part, nblk, a.N, a.dbias);
     if (e != cudaSuccess) return e;
   }
   if (a.dx) {
     GemmProblem p = {};
-    cudaError_t e = pack(a.W, a.K, a.N, &at, &p.B, s);
-    if (e != cudaSuccess) return e;
     p.A = du;
-    p.A.planes = t.dx;
+    p.A.planes = 1;
+    p.B = W;
     p.M = a.M; p.N = a.K; p.K = a.N;
     p.ep.out = a.dx;
     e = launch_gemm(p, s);
@@ -284,10 +300,8 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, void* ws, cudaStream_t s) 
   }
   if (a.dW) {
     GemmProblem p = {};
-    cudaError_t e = pack(a.x, a.M, a.K, &at, &p.A, s);
-    if (e != cudaSuccess) return e;
+    p.A = x;
     p.B = du;
-    p.B.planes = t.dW;
     p.a_mn = p.b_mn = 1;
     p.M = a.K; p.N = a.N; p.K = a.M;
     p.ep.out = a.dW;

@@ -1,5 +1,5 @@
-// linear_small.cu -- the linear layer for a few rows (decode): M <= 8.  out = x W is bound by
-// reading W once, so no tensor core is fed: each lane streams vectors of V columns of W,
+// linear_small.cu -- the linear layer for a few rows (decode): 8 to a block.  out = x W is
+// bound by reading W once, so no tensor core is fed: each lane streams vectors of V columns of W,
 // 8 of them in flight, against x in shared memory, and keeps M x V fp32 sums.  The k-range
 // is shared by a block's warps (and a warp's lane groups, where N is small) and by a cluster
 // of S blocks; sums join by shuffles, through shared memory and through distributed shared
@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(256) linear_small_kernel(const SmallArgs a) {
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tx = a.tx, G = 32 / tx, S = a.S, K = a.K, N = a.N;
+  const int m0 = blockIdx.y * 8, M = min(8, a.M - m0);
   const int rank = S > 1 ? (int)cluster_ctarank() : 0;
   const int n0 = blockIdx.x / S * (tx * V), n = n0 + (lane & (tx - 1)) * V;
   const int row = warp * G + lane / tx, rows = 8 * G;
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(256) linear_small_kernel(const SmallArgs a) {
     const int len = min(SM_KC, k1 - kc);
     for (int i = threadIdx.x; i < MB * SM_KC; i += 256) {
       const int m = i / SM_KC, k = i % SM_KC;
-      xs[m][k] = m < a.M && k < len ? __bfloat162float(__ldg(a.x + (size_t)m * K + kc + k)) : 0.0f;
+      xs[m][k] = m < M && k < len ? __bfloat162float(__ldg(a.x + (size_t)(m0 + m) * K + kc + k)) : 0.0f;
     }
     __syncthreads();
     if (n < N) {
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(256) linear_small_kernel(const SmallArgs a) {
     __syncthreads();
   }
   if (S > 1) cluster_sync();
-  for (int i = rank * 256 + threadIdx.x; i < a.M * cols; i += S * 256) {
+  for (int i = rank * 256 + threadIdx.x; i < M * cols; i += S * 256) {
     const int m = i / cols, c = i - m * cols;
     if (n0 + c >= N) continue;
     float v = 0.0f;
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(256) linear_small_kernel(const SmallArgs a) {
     } else {
       v = sums[m][c];
     }
-    finish1(a.ep, N, m, n0 + c, v);
+    finish1(a.ep, N, m0 + m, n0 + c, v);
   }
   if (S > 1) cluster_sync();                      // no block leaves while its sums are read
 }
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(256) linear_small_kernel(const SmallArgs a) {
 template <int MB, int V>
 cudaError_t run(const SmallArgs& a, int grid, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = dim3((unsigned)grid, (unsigned)cdiv(a.M, 8));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -183,11 +184,11 @@ cudaError_t launch_linear_small(const LinearArgs& l, int num_sms, cudaStream_t s
   SmallArgs a = {l.M, l.K, l.N, static_cast<const __nv_bfloat16*>(l.x), static_cast<const __nv_bfloat16*>(l.W), 1, 1, l.ep};
   const int V = a.N % 8 == 0 ? 8 : a.N % 4 == 0 ? 4 : a.N % 2 == 0 ? 2 : 1;
   while (a.tx < 32 && a.tx * V < a.N) a.tx *= 2;
-  const int tiles = cdiv(a.N, a.tx * V), rows = 8 * (32 / a.tx);
+  const int tiles = cdiv(a.N, a.tx * V) * cdiv(a.M, 8), rows = 8 * (32 / a.tx);
   // k shared by up to 8 blocks, while there are fewer than 4 blocks per SM and each lane
   // keeps its loads in flight
   while (a.S < 8 && tiles * a.S < 4 * num_sms && a.K >= a.S * 2 * rows * SM_U) a.S *= 2;
-  const int grid = tiles * a.S;
+  const int grid = cdiv(a.N, a.tx * V) * a.S;
   return V == 8 ? run_rows<8>(a, grid, s) : V == 4 ? run_rows<4>(a, grid, s) : V == 2 ? run_rows<2>(a, grid, s)
                                                                                       : run_rows<1>(a, grid, s);
 }
