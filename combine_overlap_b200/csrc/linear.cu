@@ -185,25 +185,25 @@ cudaError_t launch_dact(const LinearBwdArgs& a, int rows, int planes, __nv_bfloa
                     static_cast<const __nv_bfloat16*>(a.pre), a.M, a.N, rows, planes, du, n8, part);
 }
 
-// 32 columns per block, 8 warps each a run of the blocks' sums.
-__global__ void __launch_bounds__(256) dbias_kernel(const float* __restrict__ part, int nblk, int N,
-                                                    float* __restrict__ dbias) {
+// 32 columns per block, 32 warps each every 32nd of the blocks' sums.
+__global__ void __launch_bounds__(1024) dbias_kernel(const float* __restrict__ part, int nblk, int N,
+                                                     float* __restrict__ dbias) {
   pdl_trigger();
   pdl_wait();
-  __shared__ float sh[8][33];
+  __shared__ float sh[32][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int n = blockIdx.x * 32 + lane;
   float sum = 0.0f;
   if (n < N) {
 #pragma unroll 8
-    for (int b = w; b < nblk; b += 8) sum += part[(size_t)b * N + n];
+    for (int b = w; b < nblk; b += 32) sum += part[(size_t)b * N + n];
   }
   sh[w][lane] = sum;
   __syncthreads();
   if (w == 0 && n < N) {
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += sh[i][lane];
+    for (int i = 0; i < 32; ++i) s += sh[i][lane];
     dbias[n] = s;
   }
 }
@@ -285,7 +285,7 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, void* ws, cudaStream_t s) 
   }
   if (direct) du = {a.dout, (size_t)n8 * 2, 0, 1};
   if (a.dbias && nblk > 1) {
-    e = launch_pdl(dbias_kernel, dim3(cdiv(a.N, 32)), dim3(256), 0, s, (const float*)part, nblk, a.N, a.dbias);
+    e = launch_pdl(dbias_kernel, dim3(cdiv(a.N, 32)), dim3(1024), 0, s, (const float*)part, nblk, a.N, a.dbias);
     if (e != cudaSuccess) return e;
   }
   if (a.dx) {

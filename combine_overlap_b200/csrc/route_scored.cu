@@ -220,7 +220,7 @@ __device__ __forceinline__ void close_groups(const Plan& o, int lane, uint32_t c
 // One warp chooses one token's experts, every key and group value in 64 bits: lane
 // `slot0 + j` gets slot j's id.  k rounds of a warp-wide largest.
 template <int CM, bool FULL>
-__device__ __noinline__ int choose_f64(const Plan& o, int lane, int slot0, int my_e) {
+__device__ __noinline__ int choose_f64(const Plan o, int lane, int slot0, int my_e) {
   const int C = o.C;
   Row<CM> r;
   load_row<CM, FULL>(o.row, o.E, C, lane, r);
@@ -285,7 +285,7 @@ struct Exact {
   }
 };
 template <int CM, bool FULL>
-__device__ __noinline__ Exact exact_of(const float* __restrict__ row, int E, int softmax, int lane) {
+__device__ __forceinline__ Exact exact_of(const float* __restrict__ row, int E, int softmax, int lane) {
   Exact x = {softmax, 0.0, 1.0};
   if (softmax) {
     const int C = cdiv(E, 32);
@@ -300,6 +300,39 @@ __device__ __noinline__ Exact exact_of(const float* __restrict__ row, int E, int
     x.sum = sum > 0.0 ? sum : 1.0;
   }
   return x;
+}
+
+// The groups to choose from by their values in 64 bits.  todo: this lane's experts that may
+// be among their group's largest.
+template <int CM, bool FULL>
+__device__ __noinline__ uint32_t groups_f64(const Plan o, const float* sbias, int lane, uint32_t todo) {
+  const Exact x = exact_of<CM, FULL>(o.row, o.E, o.softmax, lane);
+  Two<double> t = {-INFINITY, -INFINITY};
+  while (__any_sync(0xffffffffu, todo != 0)) {
+    const int e = lane * o.C + __ffs(todo) - 1;
+    if (todo) t.add(x.score(fminf(__ldg(o.row + e), FLT_MAX)) + (o.bias ? (double)sbias[e] : 0.0));
+    todo &= todo - 1;
+    __syncwarp();
+  }
+  t.join_lanes(o.L);
+  uint64_t last, next, mine = 0;
+  if ((lane & (o.L - 1)) == 0 && (lane >> o.shift) < o.n_groups) mine = ordered(o.top2 && t.b != -INFINITY ? t.a + t.b : t.a);
+  return choose_groups(o, lane, mine, &last, &next);
+}
+
+// A candidate's place among n by their keys in 64 bits; me: its 32-bit key and id.
+template <int CM, bool FULL>
+__device__ __noinline__ int rank_f64(const float* __restrict__ row, int E, int softmax, const float* sbias, int lane,
+                                     int n, uint2 me) {
+  const Exact x = exact_of<CM, FULL>(row, E, softmax, lane);
+  uint64_t key = 0;
+  if (lane < n) key = me.x == 1 ? 1ull : ordered(x.score(fminf(__ldg(row + me.y), FLT_MAX)) + (double)sbias[me.y]);
+  int rank = 0;
+  for (int j = 0; j < n; ++j) {
+    const uint64_t other = __shfl_sync(0xffffffffu, key, j);
+    rank += other > key || (other == key && j < lane);
+  }
+  return rank;
 }
 
 // The same in 32 bits, with every decision checked.  A key is within err = 2^-19 (softmax) or
@@ -369,19 +402,7 @@ __device__ __forceinline__ bool choose_f32(const Row<CM>& r, const Plan& o, cons
 #pragma unroll
       for (int i = 0; i < CM; ++i)
         if ((r.live >> i & 1u) && !(v[i] < least)) todo |= 1u << i;
-      const Exact x = exact_of<CM, FULL>(o.row, o.E, o.softmax, lane);
-      Two<double> t = {-INFINITY, -INFINITY};
-      while (__any_sync(0xffffffffu, todo != 0)) {
-        const int at = __ffs(todo) - 1;
-        todo &= todo - 1;
-        if (at >= 0) t.add(x.score(fminf(__ldg(o.row + lane * C + at), FLT_MAX)) + (o.bias ? (double)sbias[lane * C + at] : 0.0));
-      }
-      __syncwarp();
-      t.join_lanes(o.L);
-      uint64_t last64, next64, mine = 0;
-      if ((lane & (o.L - 1)) == 0 && (lane >> o.shift) < o.n_groups)
-        mine = ordered(o.top2 && t.b != -INFINITY ? t.a + t.b : t.a);
-      chosen = choose_groups(o, lane, mine, &last64, &next64);
+      chosen = groups_f64<CM, FULL>(o, sbias, lane, todo);
     }
     close_groups(o, lane, chosen, key);
   }
@@ -431,14 +452,7 @@ __device__ __forceinline__ bool choose_f32(const Row<CM>& r, const Plan& o, cons
     }
     if (__any_sync(0xffffffffu, close)) {
       // in 64 bits: every candidate's key, and its place again
-      const Exact x = exact_of<CM, FULL>(o.row, o.E, o.softmax, lane);
-      uint64_t exact = 0;
-      if (lane < n) exact = me.x == 1 ? 1ull : ordered(x.score(fminf(__ldg(o.row + me.y), FLT_MAX)) + (double)sbias[me.y]);
-      rank = 0;
-      for (int j = 0; j < n; ++j) {
-        const uint64_t other = __shfl_sync(0xffffffffu, exact, j);
-        rank += other > exact || (other == exact && j < lane);
-      }
+      rank = rank_f64<CM, FULL>(o.row, o.E, o.softmax, sbias, lane, n, me);
       if (lane < n && rank < want) pool->sorted[rank] = me;
       __syncwarp();
     }

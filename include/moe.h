@@ -316,9 +316,11 @@ moe_status moe_combine_backward(const void* dout, const void* y, const int32_t* 
  * The dense products around the experts: the gate projection that makes the logits,
  * and a shared expert's up and down projections.
  *   u = x W + bias,   out = act(u) + residual
- * accumulated in fp32 and rounded once.  Any M, K, N >= 1 (rows that are not 16-byte
- * multiples are first copied into padded ones in the workspace); sums run in an
- * order that depends on the shape alone, so equal calls give equal bits. */
+ * accumulated in fp32 and rounded once.  Any M, K, N from 1 to 2^30 (rows that are no
+ * 16-byte multiples are first copied into padded ones in the workspace, unless there are
+ * few); sums run in an order that depends on the shape and the device alone, so equal
+ * calls give equal bits.  Sums of an fp32 output keep 32 bits however long they are (the
+ * tensor cores' own accumulators truncate: they hold no more than 512 products of it). */
 typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 /* erf */ } moe_act;
 typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 } moe_dtype;
 
@@ -342,10 +344,9 @@ moe_status moe_linear(const moe_linear_args* args, void* ws, size_t ws_bytes, vo
 /* The gradients:  du = dout * act'(pre),
  *   dx = du W^T,   dW = x^T du,   dbias = sum_m du      (d residual is dout itself).
  * Each output is optional.  pre is read with an activation only.  dout is bf16 or
- * fp32.  The products run on bf16 operands: an fp32 du goes in as a sum of bf16 terms
- * -- three (all 24 bits) for a dW in fp32, two for bf16 gradients, or one where the
- * product is large enough to be bound by the tensor cores (then du is rounded to
- * bf16 once, as a stored activation gradient would be). */
+ * fp32.  The products run on bf16 operands: for a dW in fp32, du goes in as a sum of three
+ * bf16 terms, which hold all 24 bits; for bf16 gradients it is rounded to bf16 once, as a
+ * stored activation gradient would be.  Without an activation a bf16 dout is du, exactly. */
 typedef struct {
   int M, K, N;
   const void* dout;         /* [M][N] of dout_dtype                                  */
