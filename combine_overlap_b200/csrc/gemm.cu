@@ -206,14 +206,20 @@ __device__ __forceinline__ void emit16(Epilogue& e, const float (&v)[32], const 
     return;
   }
   __syncwarp();
-  const int c = e.lane & 15;
+  const int c = e.lane & 15, n = cend - col - 2 * c;   // columns left from the lane's pair on
+  const bool even = (e.N & 1) == 0;
+#pragma unroll 8
   for (int i = 0; i < 16; ++i) {
     const int r = i * 2 + (e.lane >> 4);
-    if (row0 + r >= e.M) break;
     const uint32_t x = reinterpret_cast<const uint32_t*>(st + at16(r, c >> 2))[c & 3];
     unsigned short* o = static_cast<unsigned short*>(dst) + (size_t)(row0 + r) * e.N + col + 2 * c;
-    if (col + 2 * c < cend) o[0] = (unsigned short)x;
-    if (col + 2 * c + 1 < cend) o[1] = (unsigned short)(x >> 16);
+    if (row0 + r >= e.M || n <= 0) continue;
+    if (even) {
+      *reinterpret_cast<uint32_t*>(o) = x;
+    } else {
+      o[0] = (unsigned short)x;
+      if (n > 1) o[1] = (unsigned short)(x >> 16);
+    }
   }
   __syncwarp();
 }
@@ -231,10 +237,13 @@ __device__ __forceinline__ void emit32(Epilogue& e, const float (&v)[32], int ro
     return;
   }
   __syncwarp();
-  for (int r = 0; r < 32 && row0 + r < e.M; ++r)
-    if (col + e.lane < cend)
-      static_cast<float*>(e.out)[(size_t)(row0 + r) * e.N + col + e.lane] =
-          reinterpret_cast<const float*>(st + at32(r, e.lane >> 2))[e.lane & 3];
+  const bool mine = col + e.lane < cend;
+  float* o = static_cast<float*>(e.out) + (size_t)row0 * e.N + col + e.lane;
+#pragma unroll 8
+  for (int r = 0; r < 32; ++r) {
+    const float x = reinterpret_cast<const float*>(st + at32(r, e.lane >> 2))[e.lane & 3];
+    if (mine && row0 + r < e.M) o[(size_t)r * e.N] = x;
+  }
   __syncwarp();
 }
 
@@ -267,6 +276,13 @@ __device__ __forceinline__ void residual32(const Epilogue& e, int row, int col, 
         v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
         v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
       }
+    }
+  } else if ((e.N & 1) == 0) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t w = col + 2 * i < cend ? reinterpret_cast<const uint32_t*>(r)[i] : 0u;
+      v[2 * i] = __uint_as_float(w << 16);
+      v[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
     }
   } else {
 #pragma unroll
@@ -368,7 +384,7 @@ __device__ __forceinline__ void finish4(const Epilogue& e, int m, int n, float4 
 template <int S, int U>
 __device__ __forceinline__ void join_tiles(const Epilogue& e, uint32_t base, int BN, int m0, int n0, int row, int cg,
                                            int rank) {
-  constexpr int rows = 128 / S;
+  const int rows = min(128 / S, e.M - m0);
   const int per = BN / 4, pitch = (per + 1) * 16;
   uint32_t from[S];
 #pragma unroll
