@@ -945,15 +945,22 @@ Shape pick(const GemmProblem& p, int dev, int nsm) {
   return best;
 }
 
-// out = the sum of the slices, in order: one thread per 4 columns.
+// out = the sum of the slices, in order: one thread per 4 columns.  The first blocks take
+// the column sums.
 template <int U>
 __global__ void __launch_bounds__(256) join_kernel(const float4* __restrict__ ws, int SW, int M, int N, int ld4,
-                                                   void* __restrict__ out, int f32) {
+                                                   void* __restrict__ out, int f32, const ColumnSums sums) {
+  __shared__ float sh[8][33];
   pdl_trigger();
   pdl_wait();
+  const int first = sums.out ? cdiv(sums.N, 32) : 0;
+  if ((int)blockIdx.x < first) {
+    column_sums<8>(sums, blockIdx.x, sh);
+    return;
+  }
   const long total = (long)M * ld4;
   const bool vec = (N & 3) == 0;
-  for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long)gridDim.x * 256) {
+  for (long i = (long)(blockIdx.x - first) * 256 + threadIdx.x; i < total; i += (long)(gridDim.x - first) * 256) {
     float4 v = __ldcg(ws + i);
     for (int s = 1; s < SW; s += U) {
       float4 w[U];
@@ -1064,8 +1071,13 @@ cudaError_t launch_gemm(const GemmProblem& p, cudaStream_t s) {
   if (e != cudaSuccess || a.SW == 1) return e;
   const long vecs = (long)p.M * ld4;
   const int blocks = (int)(vecs < 16L * nsm * 256 ? (vecs + 255) / 256 : 16L * nsm);
-  return launch_pdl(join_kernel<4>, dim3(blocks), dim3(256), 0, s, static_cast<const float4*>(p.ws), a.SW, p.M, p.N,
-                    ld4, p.ep.out, p.ep.out_f32);
+  ColumnSums sums = {};
+  if (p.sums && p.sums->out) {
+    sums = *p.sums;
+    p.sums->out = nullptr;
+  }
+  return launch_pdl(join_kernel<4>, dim3(blocks + (sums.out ? cdiv(sums.N, 32) : 0)), dim3(256), 0, s,
+                    static_cast<const float4*>(p.ws), a.SW, p.M, p.N, ld4, p.ep.out, p.ep.out_f32, sums);
 }
 
 cudaError_t linear_timeout(cudaStream_t s, uint32_t* word) {

@@ -18,6 +18,13 @@ struct GemmOperand {
   int planes;
 };
 
+// Partial column sums [nblk][N] and where their sums go: done beside the join of slices.
+struct ColumnSums {
+  const float* part;
+  int nblk, N;
+  float* out;                    // null: none
+};
+
 struct GemmProblem {
   GemmOperand A, B;
   int a_mn, b_mn;
@@ -25,7 +32,28 @@ struct GemmProblem {
   LinearEpi ep;
   void* ws;                      // gemm_ws_bytes(M, N) for slices of the reduction, or null;
                                  // with an output alone (no bias, activation, residual, pre)
+  ColumnSums* sums;              // done if the reduction is cut into slices (out is then cleared), or null
 };
+
+// 32 columns' sums by a block of W warps: each every W-th row of partial sums.
+template <int W>
+__device__ __forceinline__ void column_sums(const ColumnSums& c, int block, float (*sh)[33]) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int n = block * 32 + lane;
+  float sum = 0.0f;
+  if (n < c.N) {
+#pragma unroll 8
+    for (int b = w; b < c.nblk; b += W) sum += c.part[(size_t)b * c.N + n];
+  }
+  sh[w][lane] = sum;
+  __syncthreads();
+  if (w == 0 && n < c.N) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) s += sh[i][lane];
+    c.out[n] = s;
+  }
+}
 
 // The current device and its SMs (asked of the driver once per device).
 cudaError_t device_of(int* dev, int* sms);

@@ -84,13 +84,14 @@ size_t pack_bytes(long rows, int n) { return n % 8 ? up256((size_t)rows * pad8(n
 // stand side by side in a row of its own: term 0 = bf16(du), term p = bf16(du - the
 // earlier terms), n8 columns each.  `part`
 // [gridDim.y][N] (optional): the block's column sums, in a fixed order.
-// Memory bounds it: the loads of DACT_R rows are issued before the first is used.  MODE: dout
+// Memory bounds it: the loads of DACT_R rows are issued before the first is used, in 4 blocks
+// per SM (8192 x 1408 with SiLU: 15.0 us with the sums; 16.9 with 4 rows and 2 blocks).  MODE: dout
 // in bf16 or fp32 with rows of 16-byte multiples, or any (element by element).
-constexpr int DACT_R = 4;
+constexpr int DACT_R = 2;
 enum { DACT_BF16, DACT_F32, DACT_ANY };
 
 template <int ACT, int MODE>
-__global__ void __launch_bounds__(256) dact_kernel(const void* __restrict__ dout, int f32,
+__global__ void __launch_bounds__(256, 4) dact_kernel(const void* __restrict__ dout, int f32,
                                                    const __nv_bfloat16* __restrict__ pre, int M,
                                                    int N, int rows, int planes, __nv_bfloat16* __restrict__ du,
                                                    int n8, float* __restrict__ part) {
@@ -185,32 +186,15 @@ cudaError_t launch_dact(const LinearBwdArgs& a, int rows, int planes, __nv_bfloa
                     static_cast<const __nv_bfloat16*>(a.pre), a.M, a.N, rows, planes, du, n8, part);
 }
 
-// 32 columns per block, 32 warps each every 32nd of the blocks' sums.
-__global__ void __launch_bounds__(1024) dbias_kernel(const float* __restrict__ part, int nblk, int N,
-                                                     float* __restrict__ dbias) {
+__global__ void __launch_bounds__(1024) dbias_kernel(const ColumnSums sums) {
+  __shared__ float sh[32][33];
   pdl_trigger();
   pdl_wait();
-  __shared__ float sh[32][33];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int n = blockIdx.x * 32 + lane;
-  float sum = 0.0f;
-  if (n < N) {
-#pragma unroll 8
-    for (int b = w; b < nblk; b += 32) sum += part[(size_t)b * N + n];
-  }
-  sh[w][lane] = sum;
-  __syncthreads();
-  if (w == 0 && n < N) {
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) s += sh[i][lane];
-    dbias[n] = s;
-  }
+  column_sums<32>(sums, blockIdx.x, sh);
 }
 
-// Rows per dact block: 16 at the least, so that a block has work; 64, DACT_R loads in
-// flight in each thread, where that leaves blocks for two waves of the device; and not so
-// few that there are more than 256 blocks of rows.
+// Rows per dact block: 16 at the least, so that a block has work; 64 where that leaves
+// blocks for every SM; and not so few that there are more than 256 blocks of rows.
 int dact_rows(int M, int N) {
   const int most = max(16, cdiv(cdiv(M, 256), 16) * 16);
   return (long long)cdiv(M, 64) * cdiv(N, 128) >= 600 ? max(64, most) : most;
@@ -284,10 +268,7 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, void* ws, cudaStream_t s) 
     if (e != cudaSuccess) return e;
   }
   if (direct) du = {a.dout, (size_t)n8 * 2, 0, 1};
-  if (a.dbias && nblk > 1) {
-    e = launch_pdl(dbias_kernel, dim3(cdiv(a.N, 32)), dim3(1024), 0, s, (const float*)part, nblk, a.N, a.dbias);
-    if (e != cudaSuccess) return e;
-  }
+  ColumnSums sums = {part, nblk, a.N, nblk > 1 ? a.dbias : nullptr};
   if (a.dx) {
     GemmProblem p = {};
     p.A = du;
@@ -307,9 +288,11 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, void* ws, cudaStream_t s) 
     p.ep.out = a.dW;
     p.ep.out_f32 = a.dW_f32;
     p.ws = at;
-    return launch_gemm(p, s);
+    p.sums = &sums;
+    e = launch_gemm(p, s);
+    if (e != cudaSuccess) return e;
   }
-  return cudaSuccess;
+  return sums.out ? launch_pdl(dbias_kernel, dim3(cdiv(a.N, 32)), dim3(1024), 0, s, sums) : cudaSuccess;
 }
 
 }  // namespace moe

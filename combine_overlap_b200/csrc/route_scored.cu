@@ -511,6 +511,7 @@ route_scored_kernel(const float* __restrict__ logits, int T, int E, int k, const
   }
   const int j = lane & 7, t = t0 + (lane >> 3) * RS_WARPS;
   const bool slot = j < k && t < T;
+  if ((unsigned)my_e >= (unsigned)E) my_e = 0;    // a bias that is not finite can leave a slot open
   const float z = slot ? __ldg(logits + (size_t)t * E + my_e) : -INFINITY;
   const bool live = z >= -FLT_MAX;
   const double zd = (double)fminf(z, FLT_MAX);
