@@ -45,6 +45,7 @@ struct GemmCtl {
   uint64_t mma_done;
   uint32_t tmem_base;
   uint32_t abort;                         // a bounded wait of this CTA ran out
+  alignas(16) float bias[G_EPI][32];                  // of each epilogue warp's chunk
 };
 
 constexpr size_t G_SMEM = 1024 + (size_t)G_RING + G_STAGING + sizeof(GemmCtl);
@@ -77,6 +78,13 @@ struct GemmArgs {
 __device__ __forceinline__ int keep(int v) { asm volatile("" : "+r"(v)); return v; }
 template <typename T>
 __device__ __forceinline__ T* keep(T* p) { asm volatile("" : "+l"(p)); return p; }
+
+// A load that stays where it stands: others sink to their first use, behind the main loop.
+__device__ __forceinline__ float ld_here(const float* p) {
+  float v;
+  asm volatile("ld.volatile.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
 
 // A converged warp waits, and leaves with one answer.  The clock is read only once a wait
 // has spun for a while: reading it costs as much as half a k-block's MMAs.
@@ -181,6 +189,7 @@ struct Epilogue {
   int act, f32;
   int M, N, lane;
   uint8_t* st;
+  float* cols;                            // 32 floats of the warp: the chunk's bias
   int turn;                               // which half of st a bf16 chunk takes next
   int part;                               // slice of the reduction (SW > 1), or 0
 };
@@ -301,8 +310,14 @@ __device__ __forceinline__ void finish_chunk(Epilogue& e, uint32_t tacc, float b
 #pragma unroll
   for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
   if (e.bias) {
+    e.cols[e.lane] = b;
+    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, b, j);
+    for (int j = 0; j < 8; ++j) {
+      const float4 c = reinterpret_cast<const float4*>(e.cols)[j];
+      v[4 * j] += c.x; v[4 * j + 1] += c.y; v[4 * j + 2] += c.z; v[4 * j + 3] += c.w;
+    }
+    __syncwarp();
   }
   if (e.pre) emit16(e, v, e.tm_pre, e.pre, row0, col, cend);
   if (e.act == 1) {
@@ -415,9 +430,9 @@ __device__ __forceinline__ void join_tiles(const Epilogue& e, uint32_t base, int
   }
 }
 
-template <bool F32>
+template <int PROMO>
 __device__ __forceinline__ Epilogue load_epilogue(const GemmArgs& a, const CUtensorMap& tm_out, const CUtensorMap& tm_pre,
-                                                  int lane, uint8_t* st) {
+                                                  int lane, uint8_t* st, float* cols) {
   Epilogue e;
   e.bias = keep(a.ep.bias);
   e.residual = keep(a.ep.residual);
@@ -426,11 +441,12 @@ __device__ __forceinline__ Epilogue load_epilogue(const GemmArgs& a, const CUten
   e.tm_out = keep(a.tma_out ? &tm_out : nullptr);
   e.tm_pre = keep(a.tma_pre ? &tm_pre : nullptr);
   e.act = keep(a.ep.act);
-  e.f32 = F32;
+  e.f32 = PROMO != 0;
   e.M = keep(a.M);
   e.N = keep(a.N);
   e.lane = lane;
   e.st = st;
+  e.cols = cols;
   e.turn = e.part = 0;
   return e;
 }
@@ -439,7 +455,9 @@ __device__ __forceinline__ Epilogue load_epilogue(const GemmArgs& a, const CUten
 // alternate pairs of chunks, so one warp writes a whole 128-byte line of bf16.
 __device__ __forceinline__ int chunk_of(int half, int i) { return ((i >> 1) * 2 + half) * 2 + (i & 1); }
 
-template <int CG, bool AMN, bool BMN, bool PROMO>
+// PROMO: chunks per epilogue warp whose sums are kept in registers (2 for BN <= 128: with 4
+// the sums leave too few registers, and the epilogue's own spill), or 0.
+template <int CG, bool AMN, bool BMN, int PROMO>
 __global__ void __launch_bounds__(G_THREADS, 1)
 gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
             const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ CUtensorMap tm_pre,
@@ -636,7 +654,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
     const int q = warp & 3, half = (warp - 2) >> 2;   // TMEM lanes 32 q ..
     int acc = 0;
     uint32_t aph = 0;
-    Epilogue ep = load_epilogue<PROMO>(a, tm_out, tm_pre, lane, staging + (warp - 2) * 4096);
+    Epilogue ep = load_epilogue<PROMO>(a, tm_out, tm_pre, lane, staging + (warp - 2) * 4096, ctl->bias[warp - 2]);
     const int BN = keep(a.BN);
     const bool low = a.PB > 1;
     bool ok = true;
@@ -660,14 +678,14 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int c = chunk_of(half, i) * 32 + lane;
-          if (c < BN && n0 + c < ep.N) b[i] = __ldg(ep.bias + n0 + c);
+          if (c < BN && n0 + c < ep.N) b[i] = ld_here(ep.bias + n0 + c);
         }
       }
-      float sum[PROMO ? 4 : 1][32];
+      float sum[PROMO ? PROMO : 1][32];
       // sum (+)= this warp's chunks of the accumulator at `tb`
       auto promote = [&](uint32_t tb, bool first) {
 #pragma unroll
-        for (int i = 0; i < (PROMO ? 4 : 0); ++i) {
+        for (int i = 0; i < PROMO; ++i) {
           const int ch = chunk_of(half, i);
           if (ch * 32 < BN) {
             uint32_t r[32];
@@ -684,7 +702,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
         }
         if (low) {                        // BN <= 128
 #pragma unroll
-          for (int i = 0; i < (PROMO ? 2 : 0); ++i) {
+          for (int i = 0; i < min(PROMO, 2); ++i) {
             const int ch = chunk_of(half, i);
             if (ch * 32 < BN) {
               uint32_t r[32];
@@ -696,7 +714,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
           }
         }
       };
-      if constexpr (PROMO) {
+      if constexpr (PROMO != 0) {
         for (int c = 0; c + 1 < nch && ok; ++c) {
           if (!g_wait<CG>(&ctl->tfull[acc], aph, ctl)) { ok = false; break; }
           tc_fence_after();
@@ -709,12 +727,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
       if (!ok || !g_wait<CG>(&ctl->tfull[acc], aph, ctl)) { ok = false; break; }
       tc_fence_after();
       const uint32_t tb = lanes + (uint32_t)(acc * ACC_COLS);
-      if constexpr (PROMO) {
+      if constexpr (PROMO != 0) {
         if (nch > 1 || low) {
           // the last chain joins the sums, and the sums go where the code below reads
           promote(tb, nch == 1);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < PROMO; ++i) {
             const int ch = chunk_of(half, i);
             if (ch * 32 < BN) {
               uint32_t r[32];
@@ -759,7 +777,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
     if (!*reinterpret_cast<volatile uint32_t*>(&ctl->abort)) {
       int tm, tn;
       tile_at(a, t0, &tm, &tn);
-      const Epilogue ep = load_epilogue<PROMO>(a, tm_out, tm_pre, lane, staging);
+      const Epilogue ep = load_epilogue<PROMO>(a, tm_out, tm_pre, lane, staging, nullptr);
       const int row = split * (128 / S), m0 = tm * (128 * CG) + rank * 128 + row, n0 = tn * a.BN;
       if (S == 2) join_tiles<2, 4>(ep, smem_u32(smem), a.BN, m0, n0, row, CG, rank);
       else if (S == 4) join_tiles<4, 2>(ep, smem_u32(smem), a.BN, m0, n0, row, CG, rank);
@@ -828,7 +846,7 @@ bool encode_out(CUtensorMap* m, void* p, int M, int N, int ld, int slices, int f
             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int CG, bool AMN, bool BMN, bool PROMO>
+template <int CG, bool AMN, bool BMN, int PROMO>
 cudaError_t run(const CUtensorMap (&m)[4], const GemmArgs& a, int grid, int dev, cudaStream_t s) {
   static bool configured[64] = {false};
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -855,13 +873,13 @@ cudaError_t run(const CUtensorMap (&m)[4], const GemmArgs& a, int grid, int dev,
   return cudaLaunchKernelEx(&cfg, gemm_kernel<CG, AMN, BMN, PROMO>, m[0], m[1], m[2], m[3], a);
 }
 
-template <int CG, bool PROMO>
+template <int CG, int PROMO>
 cudaError_t run_major(const GemmProblem& p, const CUtensorMap (&m)[4], const GemmArgs& a, int grid, int dev,
                       cudaStream_t s) {
   if (p.a_mn) return p.b_mn ? run<CG, true, true, PROMO>(m, a, grid, dev, s) : cudaErrorInvalidValue;
   if (p.b_mn) return run<CG, false, true, PROMO>(m, a, grid, dev, s);
-  if constexpr (PROMO) return cudaErrorInvalidValue;   // no product of the layer has an fp32 output here
-  else return run<CG, false, false, false>(m, a, grid, dev, s);
+  if constexpr (PROMO != 0) return cudaErrorInvalidValue;   // no product of the layer has an fp32 output here
+  else return run<CG, false, false, 0>(m, a, grid, dev, s);
 }
 
 // SM cycles of one tile configuration, from rates measured on one B200: an MMA of
@@ -887,7 +905,7 @@ int clusters_of(int dev, int nsm, int size) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int n = 0;
-    auto kernel = gemm_kernel<2, false, true, false>;
+    auto kernel = gemm_kernel<2, false, true, 0>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G_SMEM) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
       cudaGetLastError();
@@ -1066,8 +1084,12 @@ cudaError_t launch_gemm(const GemmProblem& p, cudaStream_t s) {
   }
   if (a.tma_pre && !encode_out(&m[3], p.ep.pre, p.M, p.N, p.N, 1, 0)) return cudaErrorInvalidValue;
   const int grid = c.CG * (a.S > 1 ? ntiles * a.S : min(ntiles * a.SW, clusters_of(dev, nsm, c.CG)));
-  if (c.CG == 2) e = promo ? run_major<2, true>(p, m, a, grid, dev, s) : run_major<2, false>(p, m, a, grid, dev, s);
-  else e = promo ? run_major<1, true>(p, m, a, grid, dev, s) : run_major<1, false>(p, m, a, grid, dev, s);
+  if (c.CG == 2)
+    e = !promo ? run_major<2, 0>(p, m, a, grid, dev, s)
+        : a.BN <= 128 ? run_major<2, 2>(p, m, a, grid, dev, s) : run_major<2, 4>(p, m, a, grid, dev, s);
+  else
+    e = !promo ? run_major<1, 0>(p, m, a, grid, dev, s)
+        : a.BN <= 128 ? run_major<1, 2>(p, m, a, grid, dev, s) : run_major<1, 4>(p, m, a, grid, dev, s);
   if (e != cudaSuccess || a.SW == 1) return e;
   const long vecs = (long)p.M * ld4;
   const int blocks = (int)(vecs < 16L * nsm * 256 ? (vecs + 255) / 256 : 16L * nsm);
