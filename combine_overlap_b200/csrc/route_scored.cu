@@ -14,8 +14,9 @@ constexpr int RS_WARPS = 8;                       // warps per block; ROUTE_TOK 
 constexpr int RS_TOK = ROUTE_TOK / RS_WARPS;
 static_assert(RS_TOK * MAX_K <= 32, "a lane for each slot of a warp's tokens");
 
-// Keys as unsigned integers of the same order; 0: not to be chosen, 1: masked (after every
-// live expert, before none), so a warp's largest is one redux instruction away.
+// Keys as unsigned integers of the same order, so a warp's largest is one redux instruction
+// away; 0: not to be chosen; a masked expert comes after every live one: 1, or in 32 bits
+// MASKED, the key of -infinity.
 __device__ __forceinline__ uint32_t ordered(float f) {
   const uint32_t u = __float_as_uint(f + 0.0f);   // -0 and 0 are one key
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
@@ -24,6 +25,7 @@ __device__ __forceinline__ uint64_t ordered(double f) {
   const uint64_t u = (uint64_t)__double_as_longlong(f + 0.0);
   return u ^ ((u >> 63) ? ~0ull : 1ull << 63);
 }
+constexpr uint32_t MASKED = 0x007fffffu;
 __device__ __forceinline__ float unordered(uint32_t u) { return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu)); }
 
 // exp(x) and 1 / x, a few units in the last place off; what underflows is 0.
@@ -134,6 +136,14 @@ __device__ __forceinline__ float top_row(const Row<CM>& r) {
     if (r.live >> i & 1u) m = max(m, ordered(r.z[i]));
   m = warp_max(m);
   return m ? unordered(m) : -FLT_MAX;
+}
+// The same of z with -infinity for what is masked; never -infinity itself.
+template <int CM>
+__device__ __forceinline__ float top_of(const float (&z)[CM]) {
+  float m = z[0];
+#pragma unroll
+  for (int i = 1; i < CM; ++i) m = fmaxf(m, z[i]);
+  return fmaxf(unordered(warp_max(ordered(m))), -FLT_MAX);
 }
 template <int CM>
 __device__ __forceinline__ void softmax_row(const Row<CM>& r, float (&ex)[CM], float* top, float* sum) {
@@ -326,7 +336,7 @@ __device__ __noinline__ int rank_f64(const float* __restrict__ row, int E, int s
                                      int n, uint2 me) {
   const Exact x = exact_of<CM, FULL>(row, E, softmax, lane);
   uint64_t key = 0;
-  if (lane < n) key = me.x == 1 ? 1ull : ordered(x.score(fminf(__ldg(row + me.y), FLT_MAX)) + (double)sbias[me.y]);
+  if (lane < n) key = me.x <= MASKED ? 1ull : ordered(x.score(fminf(__ldg(row + me.y), FLT_MAX)) + (double)sbias[me.y]);
   int rank = 0;
   for (int j = 0; j < n; ++j) {
     const uint64_t other = __shfl_sync(0xffffffffu, key, j);
@@ -348,19 +358,17 @@ __device__ __noinline__ int rank_f64(const float* __restrict__ row, int E, int s
 // 12 of 256 experts) goes to a lane each, in the order of ids, and finds its place by
 // comparing itself with all the others.
 template <int CM, bool FULL>
-__device__ __forceinline__ bool choose_f32(const Row<CM>& r, const Plan& o, const float* sbias, int lane, int slot0,
-                                           Pool* pool, int* my_e) {
+__device__ __forceinline__ bool choose_f32(const float (&z)[CM], const Plan& o, const float* sbias, float err, int lane,
+                                           int slot0, Pool* pool, int* my_e) {
   const int C = FULL ? CM : o.C;
-  float v[CM];
-  float err = 0.0f;
+  float v[CM];                                    // p + bias, or the logits; -infinity: masked
   if (o.scores) {
-    float reach = 0.0f;                           // the largest |p + bias|
     if (o.softmax) {
-      const float top = top_row<CM>(r);
+      const float top = top_of<CM>(z);
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < CM; ++i) {
-        v[i] = (r.live >> i & 1u) ? exp_fast(r.z[i] - top) : 0.0f;
+        v[i] = exp_fast(z[i] - top);
         sum += v[i];
       }
       sum = warp_sum(sum);
@@ -369,39 +377,46 @@ __device__ __forceinline__ bool choose_f32(const Row<CM>& r, const Plan& o, cons
       for (int i = 0; i < CM; ++i) v[i] *= inv;
     } else {
 #pragma unroll
-      for (int i = 0; i < CM; ++i) v[i] = rcp_fast(1.0f + exp_fast(-r.z[i]));
+      for (int i = 0; i < CM; ++i) v[i] = rcp_fast(1.0f + exp_fast(-z[i]));
     }
     if (o.bias) {
+      if constexpr (FULL && CM >= 4) {
 #pragma unroll
-      for (int i = 0; i < CM; ++i)
-        if (r.live >> i & 1u) v[i] += sbias[lane * C + i];
+        for (int i = 0; i < CM / 4; ++i) {
+          const float4 b = reinterpret_cast<const float4*>(sbias + lane * CM)[i];
+          v[4 * i] += b.x; v[4 * i + 1] += b.y; v[4 * i + 2] += b.z; v[4 * i + 3] += b.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < CM; ++i)
+          if (z[i] != -INFINITY) v[i] += sbias[lane * C + i];
+      }
     }
 #pragma unroll
-    for (int i = 0; i < CM; ++i)
-      if (r.live >> i & 1u) reach = fmaxf(reach, fabsf(v[i]));
-    reach = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(reach)));
-    err = (o.softmax ? 1.91e-6f : 4.77e-7f) + 1.2e-7f * reach;
+    for (int i = 0; i < CM; ++i) v[i] = z[i] == -INFINITY ? -INFINITY : v[i];
   } else {
 #pragma unroll
-    for (int i = 0; i < CM; ++i) v[i] = r.z[i];
+    for (int i = 0; i < CM; ++i) v[i] = z[i];
   }
   uint32_t key[CM];
 #pragma unroll
-  for (int i = 0; i < CM; ++i)
-    key[i] = (r.live >> i & 1u) ? ordered(o.bias ? v[i] : r.z[i]) : FULL ? 1u : (r.have >> i & 1u);
+  for (int i = 0; i < CM; ++i) {
+    key[i] = ordered(o.bias ? v[i] : z[i]);
+    if (!FULL && !(i < C && lane * C + i < o.E)) key[i] = 0;
+  }
   if (o.grouped) {
     uint32_t last = 0, next = 0;
     Two<float> seen = {0.0f, 0.0f};
-    uint32_t chosen = choose_groups(o, lane, group_values<uint32_t>(o, lane, v, r.live, &seen), &last, &next);
+    uint32_t chosen = choose_groups(o, lane, group_values<uint32_t>(o, lane, v, ~0u, &seen), &last, &next);
     // a group's value has the errors of two keys and of their sum
-    if (o.scores && next > ordered(-INFINITY) && !(unordered(last) - unordered(next) > 6.0f * err)) {
+    if (o.scores && next > MASKED && !(unordered(last) - unordered(next) > 6.0f * err)) {
       if (!o.L) return false;
       // in 64 bits: the experts that may be among their group's largest
       const float least = (o.top2 && seen.b != -INFINITY ? seen.b : seen.a) - 2.0f * err;
       uint32_t todo = 0;
 #pragma unroll
       for (int i = 0; i < CM; ++i)
-        if ((r.live >> i & 1u) && !(v[i] < least)) todo |= 1u << i;
+        if (v[i] != -INFINITY && !(v[i] < least)) todo |= 1u << i;
       chosen = groups_f64<CM, FULL>(o, sbias, lane, todo);
     }
     close_groups(o, lane, chosen, key);
@@ -415,7 +430,7 @@ __device__ __forceinline__ bool choose_f32(const Row<CM>& r, const Plan& o, cons
     if (best == floor) best = 0;                  // ties go at once: the floor is only lower for it
   }
   // no lanes left: every open expert may be needed; with a bias what is as good as the floor
-  if (o.bias && floor > 1) floor = ordered(unordered(floor) - 2.0f * err);
+  if (o.bias && floor > MASKED) floor = ordered(unordered(floor) - 2.0f * err);
   floor = max(floor, 1u);
   uint32_t in = 0;
 #pragma unroll
@@ -448,7 +463,7 @@ __device__ __forceinline__ bool choose_f32(const Row<CM>& r, const Plan& o, cons
     bool close = false;
     if (lane + 1 < min(want, n)) {
       const uint32_t a = pool->sorted[lane].x, b = pool->sorted[lane + 1].x;
-      close = b > 1 && !(unordered(a) - unordered(b) > 2.0f * err);
+      close = b > MASKED && !(unordered(a) - unordered(b) > 2.0f * err);
     }
     if (__any_sync(0xffffffffu, close)) {
       // in 64 bits: every candidate's key, and its place again
@@ -485,6 +500,12 @@ route_scored_kernel(const float* __restrict__ logits, int T, int E, int k, const
   __shared__ Pool pools[RS_WARPS];
   Pool* pool = &pools[warp];
   Plan plan = plan_of(E, k, o);
+  float reach = 0.0f;                             // the largest |bias|: a key is no further out than that and 1
+  if (o.bias) {
+    for (int e = lane; e < E; e += 32) reach = fmaxf(reach, fabsf(sbias[e]));
+    reach = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(reach)));
+  }
+  const float err = !plan.scores ? 0.0f : (plan.softmax ? 1.91e-6f : 4.77e-7f) + 1.2e-7f * (1.0f + reach);
   const int t0 = blockIdx.x * ROUTE_TOK + warp;   // its tokens: t0, t0 + 8, ..
   int my_e = 0;
   float my_top = 0.0f, my_sum = 1.0f;
@@ -494,14 +515,24 @@ route_scored_kernel(const float* __restrict__ logits, int T, int E, int k, const
     if (t >= T) break;
     Row<CM> r;
     load_row<CM, FULL>(logits + (size_t)t * E, E, C, lane, r);
-    mask_row<CM, FULL>(E, C, lane, r);
+    float z[CM];
+#pragma unroll
+    for (int i = 0; i < CM; ++i) {
+      const bool have = FULL || (i < C && lane * C + i < E);
+      z[i] = have && r.z[i] >= -FLT_MAX ? fminf(r.z[i], FLT_MAX) : -INFINITY;   // NaN and -infinity: masked
+    }
     plan.row = logits + (size_t)t * E;
-    if (!choose_f32<CM, FULL>(r, plan, sbias, lane, q * MAX_K, pool, &my_e))
+    if (!choose_f32<CM, FULL>(z, plan, sbias, err, lane, q * MAX_K, pool, &my_e))
       my_e = choose_f64<CM, FULL>(plan, lane, q * MAX_K, my_e);
     if (o.score == 0) {
-      float ex[CM], top, sum = 1.0f;
-      if (o.renorm) top = top_row<CM>(r);         // the sum cancels
-      else softmax_row<CM>(r, ex, &top, &sum);
+      const float top = top_of<CM>(z);
+      float sum = 1.0f;
+      if (!o.renorm) {                            // else the sum cancels
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < CM; ++i) sum += expf(z[i] - top);
+        sum = warp_sum(sum);
+      }
       if (lane >> 3 == q) { my_top = top; my_sum = sum; }
     }
     if (lane == 0) {
