@@ -564,9 +564,12 @@ route_scored_kernel(const float* __restrict__ logits, int T, int E, int k, const
 }
 
 // The gradient.  With w the chosen scores, S their sum and c_j = scale * dgate_j:
-//   dp_j = c_j, or (c_j - sum_i c_i w_i / S) / S with renorm;
-//   softmax: dz_e = p_e (dp_e - sum_j p_j dp_j);  sigmoid: dz_e = dp_e p_e (1 - p_e).
-// With renorm the softmax's own normaliser cancels, and dz is 0 beside the chosen.
+//   softmax: dz_e = p_e (c_e - sum_j w_j c_j), c_e = 0 beside the chosen;
+//   sigmoid: dz_e = c_e p_e (1 - p_e);
+//   with renorm and the shares q_j = w_j / S: dz_e = q_e (c_e - sum_j q_j c_j), for the sigmoid
+//   times 1 - p_e.  The softmax's own normaliser cancels, and dz is 0 beside the chosen.
+// Shares, not scores over S^2: 1 / S overflows where the chosen scores are below 2^-1024, and
+// where one expert has the whole sum its share is 1 and the gradient exactly 0.
 // A warp takes 4 tokens: lane 8 q + j is token q's slot j, in 64 bits; then the warp
 // writes the 4 rows, and the slots their experts' values over them.  `zero`: there is
 // nothing beside the chosen.
@@ -610,13 +613,13 @@ route_scored_bwd_kernel(const float* __restrict__ dgate, const float* __restrict
   if (live) w = exp(o.score == 0 ? zd - (double)my_top : -zd);
   if (o.score == 0) w /= (double)my_sum;
   else w = live ? 1.0 / (1.0 + w) : 0.0;
-  double dp = c;
+  double share = w;
   if (o.renorm) {
-    const double S = sum8(w), cw = sum8(c * w);
-    dp = S > 0.0 ? (c - cw / S) / S : 0.0;
+    const double S = sum8(w);
+    share = S > 0.0 ? w / S : 0.0;
   }
-  const double dot = zero ? 0.0 : sum8(w * dp);
-  const float dz = live ? (float)(o.score == 0 ? w * (dp - dot) : dp * w * (1.0 - w)) : 0.0f;
+  const double dot = o.score == 0 || o.renorm ? sum8(share * c) : 0.0;
+  const float dz = live ? (float)(share * (c - dot) * (o.score == 0 ? 1.0 : 1.0 - w)) : 0.0f;
   if (zero) {
     // 4 rows of zeros in one run
     const int rows = min(4, T - t0), n = rows * E;

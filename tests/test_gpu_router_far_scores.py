@@ -1,0 +1,63 @@
+"""The router's gates and their gradient where scores are very small or gates constant,
+against the formulas with the chosen experts' own largest logit as the reference of the
+exponentials (the softmax's normaliser cancels when gates are renormalised)."""
+import numpy as np
+import pytest
+import torch
+
+import router_ref as ref
+
+pytestmark = pytest.mark.gpu
+moe = pytest.importorskip("combine_overlap_b200.moe")
+
+
+def _backward(dg, z, idx, kind, scale=1.0):
+    return moe.route_scored_backward(torch.from_numpy(dg).cuda(), torch.from_numpy(z).cuda(),
+                                     torch.from_numpy(idx.astype(np.int32)).cuda(), score=kind, renorm=True,
+                                     scale=scale).cpu().double().numpy()
+
+
+def _shares(z, idx, kind):
+    """The chosen experts' shares w / S, row by row, without the softmax's normaliser."""
+    s = np.take_along_axis(z.astype(np.float64), idx, 1)
+    w = np.exp(s - s.max(1, keepdims=True))
+    if kind == 1:                          # sigmoid(s) = exp(s) / (1 + exp(s))
+        w /= 1 + np.exp(s)
+    return w / w.sum(1, keepdims=True), s
+
+
+def _gradient(dg, z, idx, kind, scale=1.0):
+    q, s = _shares(z, idx, kind)
+    c = scale * dg.astype(np.float64)
+    d = q * (c - (q * c).sum(1, keepdims=True))
+    if kind == 1:
+        d /= 1 + np.exp(s)                 # 1 - sigmoid(s)
+    dz = np.zeros(z.shape)
+    np.put_along_axis(dz, idx, d, 1)
+    # one rounding to fp32; shares of 64 bits, subnormal ones (from 2^-1029 on) of 44 and more
+    return dz, ref.F32 * np.abs(dz) + 1e-12 * np.abs(c).sum(1, keepdims=True) * (dz != 0)
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("scale", [1.0, 2.5])
+def test_a_constant_gate_has_no_gradient(kind, scale):
+    """A renormalised gate of one expert is `scale` whatever the logits: 0, and no rounding of it."""
+    rng = np.random.default_rng(kind)
+    z = (3 * rng.normal(size=(2000, 24))).astype(np.float32)
+    dg = rng.normal(size=(2000, 1)).astype(np.float32)
+    assert not _backward(dg, z, ref.route(z, 1, kind)[0].astype(int), kind, scale).any()
+    z[:, 1:] = -np.inf                     # one live expert among three chosen
+    dg = rng.normal(size=(2000, 3)).astype(np.float32)
+    assert not _backward(dg, z, np.tile([0, 1, 2], (2000, 1)), kind, scale).any()
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+def test_gradients_of_sums_whose_reciprocal_overflows(kind):
+    """The chosen scores' sum below 2^-1024: by a bias, a group limit or the caller's ids."""
+    low = np.array([-709.0, -709.5, -709.2, -709.7]) - (0 if kind else 2)
+    z = np.stack([np.r_[0, low, -5], np.r_[0, low[::-1], 1], np.r_[0, low - 0.05, -800]]).astype(np.float32)
+    idx = np.array([[1, 2, 3], [4, 1, 2], [3, 4, 1]])
+    dg = np.array([[2.5, -5, 1], [1, 1, -3], [0.1, 7, 1]], np.float32)
+    want, bound = _gradient(dg, z, idx, kind)
+    got = _backward(dg, z, idx, kind)
+    assert np.abs(want).max() > 0.5 and np.all(np.abs(got - want) <= bound), (got, want)
