@@ -64,7 +64,7 @@ cudaError_t launch_gemm(const GemmProblem& p, cudaStream_t s);
 
 __device__ __forceinline__ float act_f32(int act, float u) {
   switch (act) {
-    case 1: return fmaxf(u, 0.0f);
+    case 1: return u < 0.0f ? 0.0f : u;   // a NaN stays one
     case 2: return __fdividef(u, 1.0f + __expf(-u));
     case 3: return 0.5f * u * (1.0f + erff(u * 0.70710678f));
   }
