@@ -46,6 +46,28 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t v) {
   const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
   return (uint64_t)hi << 32 | lo;
 }
+// Over the 8 lanes of a token's slots.
+template <typename F>
+__device__ __forceinline__ F sum8(F v) {
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+__device__ __forceinline__ float max8(float v) {
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+  return v;
+}
+
+// What a softmax's renormalised shares take their exponentials from: the largest chosen
+// logit, since the softmax's own normaliser cancels.  From the row's largest they lose their
+// bits as subnormals where a bias or a group limit leaves only experts 708 and more below
+// it.  Scores are 64-bit values, which end 745.13 below: what is all beyond that is 0.
+__device__ __forceinline__ float share_top(float z, bool live, float row_top) {
+  const float top = max8(live ? fminf(z, FLT_MAX) : -FLT_MAX);
+  return (double)top - (double)row_top < -745.13 ? INFINITY : top;
+}
+
 template <typename F>
 __device__ __forceinline__ F warp_sum(F v) {
 #pragma unroll
@@ -546,12 +568,11 @@ route_scored_kernel(const float* __restrict__ logits, int T, int E, int k, const
   const float z = slot ? __ldg(logits + (size_t)t * E + my_e) : -INFINITY;
   const bool live = z >= -FLT_MAX;
   const double zd = (double)fminf(z, FLT_MAX);
+  if (o.score == 0 && o.renorm) my_top = share_top(z, live, my_top);
   double w = 0.0;
   if (live) w = exp(o.score == 0 ? zd - (double)my_top : -zd);
   if (o.score != 0) w = live ? 1.0 / (1.0 + w) : 0.0;
-  double total = w;                               // over the token's slots
-#pragma unroll
-  for (int off = 4; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+  double total = sum8(w);                         // over the token's slots
   if (!o.renorm) total = o.score == 0 ? (double)my_sum : 1.0;
   if (slot) {
     topk_idx[(size_t)t * k + j] = my_e;
@@ -604,11 +625,7 @@ route_scored_bwd_kernel(const float* __restrict__ dgate, const float* __restrict
       if (lane >> 3 == q) { my_top = top; my_sum = sum > 0.0f ? sum : 1.0f; }
     }
   }
-  auto sum8 = [](double v) {
-#pragma unroll
-    for (int off = 4; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    return v;
-  };
+  if (o.score == 0 && o.renorm) my_top = share_top(z, live, my_top);
   double w = 0.0;
   if (live) w = exp(o.score == 0 ? zd - (double)my_top : -zd);
   if (o.score == 0) w /= (double)my_sum;

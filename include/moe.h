@@ -262,7 +262,8 @@ moe_status moe_layer_forward(const moe_layer_args* args, moe_mode mode,
  *   chosen the k largest keys, by key descending; keys and group values are compared
  *          as 64-bit values, ties go to the lower expert (group) id
  *   gate   scale * p_e, or scale * p_e / (sum of the k chosen p) with renorm
- *          (0 where that sum is 0).
+ *          (0 where that sum is 0: a softmax score is 0 from 745.13 below the row's
+ *          largest logit on, a sigmoid's from -709.78 on).
  * A logit of -infinity or NaN masks its expert: its score is 0, it comes after every
  * other expert of the chosen groups (by id), a group counts its other experts only
  * and a group of masked experts comes last; a token with fewer than k experts left

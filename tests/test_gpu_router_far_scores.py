@@ -61,3 +61,39 @@ def test_gradients_of_sums_whose_reciprocal_overflows(kind):
     want, bound = _gradient(dg, z, idx, kind)
     got = _backward(dg, z, idx, kind)
     assert np.abs(want).max() > 0.5 and np.all(np.abs(got - want) <= bound), (got, want)
+
+
+FAR = np.array([-715, -716, -714.5, -717, -730, -730.25, -731, -729.5, -743, -744, -744.5, -742], np.float32).reshape(3, 4)
+
+
+def test_shares_of_experts_far_below_the_largest():
+    """Softmax gates of experts 714 to 744 below the row's largest, which a bias leaves out:
+    their scores are subnormal in 64 bits, their shares are not."""
+    z = np.concatenate([np.zeros((3, 1), np.float32), FAR], 1)
+    bias = np.array([-9, 0.4, 0.3, 0.2, 0.1], np.float32)
+    dg = np.array([[1, -2, 0.5], [3, 1, -1], [0.25, 2, 1]], np.float32)
+    idx, gate = moe.route_scored(torch.from_numpy(z).cuda(), 3, bias=torch.from_numpy(bias).cuda(), scale=1.5)
+    chosen = np.tile([1, 2, 3], (3, 1))
+    assert np.array_equal(idx.cpu().numpy(), chosen)
+    q, _ = _shares(z, chosen, 0)
+    # one rounding to fp32, and 64-bit ones
+    assert np.all(np.abs(gate.cpu().double().numpy() - 1.5 * q) <= ref.F32 * 1.5 * q * 1.0001)
+    want, bound = _gradient(dg, z, chosen, 0, 1.5)
+    assert np.all(np.abs(_backward(dg, z, chosen, 0, 1.5) - want) <= bound)
+
+
+def test_scores_that_underflow_have_neither_gate_nor_gradient():
+    """All chosen more than 745.13 below: their sum is 0 in 64 bits, and so are the gates."""
+    z = np.array([[0, -746, -747, -748], [0, -746, -1e30, -np.inf], [1e38, 5, 6, 7]], np.float32)
+    bias = np.array([-9, 0.4, 0.3, 0.2], np.float32)
+    dg = np.ones((3, 2), np.float32)
+    idx, gate = moe.route_scored(torch.from_numpy(z).cuda(), 2, bias=torch.from_numpy(bias).cuda())
+    assert (idx.cpu().numpy() == [1, 2]).all() and not gate.any()
+    assert not _backward(dg, z, idx.cpu().numpy(), 0).any()
+    # one of them inside: it has the whole sum
+    z[:, 1] = z[:, 0] + np.float32(-744)
+    z[2, 0] = 1e4
+    z[2, 1:] = [1e4 - 744, 5, 6]
+    idx, gate = moe.route_scored(torch.from_numpy(z).cuda(), 2, bias=torch.from_numpy(bias).cuda())
+    want = np.array([[np.exp(3.0) / (1 + np.exp(3.0)), 1 / (1 + np.exp(3.0))], [1, 0], [1, 0]])   # -744 and -747
+    assert np.all(np.abs(gate.cpu().double().numpy() - want) <= ref.F32 * want * 1.0001)
