@@ -609,8 +609,9 @@ route_scored_bwd_kernel(const float* __restrict__ dgate, const float* __restrict
   int e = slot ? topk_idx[(size_t)t * k + j] : -1;
   if ((unsigned)e >= (unsigned)E) e = -1;
   const float z = e >= 0 ? __ldg(logits + (size_t)t * E + e) : -INFINITY;
-  const double c = e >= 0 ? (double)o.scale * (double)dgate[(size_t)t * k + j] : 0.0;
   const bool live = z >= -FLT_MAX;
+  // a masked expert's gate is the constant 0: what its dgate holds, NaN or not, counts for nothing
+  const double c = live ? (double)o.scale * (double)dgate[(size_t)t * k + j] : 0.0;
   const double zd = (double)fminf(z, FLT_MAX);
   const bool zero = o.score != 0 || o.renorm;
   float my_top = 0.0f, my_sum = 1.0f;

@@ -291,10 +291,11 @@ moe_status moe_route_scored(const float* logits, int T, int E, int k, const moe_
 
 /* The gradient of moe_route_scored's gates: dgate [T][k] fp32 and the forward's
  * logits and topk_idx -> dlogits [T][E] fp32 (every element is written).  The choice
- * itself has no gradient, nor has the bias; masked experts get 0, and so does a row
- * whose renormalising sum is 0 or one expert's alone (its gate is `scale`, whatever the
- * logits: k = 1 with renorm has a gradient of exactly 0).  A topk_idx outside [0, E) is skipped (a dropped
- * slot); an id may stand in a row once only.  Of the router, score, renorm and scale
+ * itself has no gradient, nor has the bias; masked experts get 0 whatever their dgate
+ * holds, and so does a row whose renormalising sum is 0 or one expert's alone (its gate
+ * is `scale`, whatever the logits: k = 1 with renorm has a gradient of exactly 0).  A
+ * topk_idx outside [0, E) is skipped (a dropped slot; the sum is over the others); an id
+ * may stand in a row once only.  Of the router, score, renorm and scale
  * are read. */
 moe_status moe_route_scored_backward(const float* dgate, const float* logits,
                                      const int32_t* topk_idx, int T, int E, int k,

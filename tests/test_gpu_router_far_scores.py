@@ -97,3 +97,23 @@ def test_scores_that_underflow_have_neither_gate_nor_gradient():
     idx, gate = moe.route_scored(torch.from_numpy(z).cuda(), 2, bias=torch.from_numpy(bias).cuda())
     want = np.array([[np.exp(3.0) / (1 + np.exp(3.0)), 1 / (1 + np.exp(3.0))], [1, 0], [1, 0]])   # -744 and -747
     assert np.all(np.abs(gate.cpu().double().numpy() - want) <= ref.F32 * want * 1.0001)
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_gradients_of_masked_and_dropped_slots_are_not_read(kind, renorm, what):
+    """NaN and infinities in dgate where the expert is masked or the slot dropped reach nothing."""
+    rng = np.random.default_rng(5)
+    z = rng.normal(size=(64, 40)).astype(np.float32)
+    z[::2, 3:] = -np.inf                   # three live experts among five chosen
+    z[5], z[6] = -np.inf, np.nan
+    idx = ref.route(z, 5, kind)[0]
+    idx[9, 2], idx[11, 4] = -1, 40
+    dg = rng.normal(size=(64, 5)).astype(np.float32)
+    inside = (idx >= 0) & (idx < 40)
+    used = inside & np.isfinite(np.take_along_axis(z, np.where(inside, idx, 0).astype(int), 1))
+    run = lambda d: moe.route_scored_backward(torch.from_numpy(d).cuda(), torch.from_numpy(z).cuda(),  # noqa: E731
+                                              torch.from_numpy(idx).cuda(), score=kind, renorm=renorm)
+    want, got = run(np.where(used, dg, np.float32(0))), run(np.where(used, dg, np.float32(what)))
+    assert not used.all() and torch.isfinite(want).all() and torch.equal(got, want)
