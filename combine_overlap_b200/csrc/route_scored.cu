@@ -629,15 +629,21 @@ route_scored_bwd_kernel(const float* __restrict__ dgate, const float* __restrict
   if (o.score == 0 && o.renorm) my_top = share_top(z, live, my_top);
   double w = 0.0;
   if (live) w = exp(o.score == 0 ? zd - (double)my_top : -zd);
-  if (o.score == 0) w /= (double)my_sum;
-  else w = live ? 1.0 / (1.0 + w) : 0.0;
+  double rest = 1.0;                              // sigmoid: 1 - p, from the exponential where p is near 1
+  if (o.score == 0) {
+    w /= (double)my_sum;
+  } else {
+    const double x = w;
+    w = live ? 1.0 / (1.0 + x) : 0.0;
+    rest = w < 0.5 ? 1.0 - w : x * w;
+  }
   double share = w;
   if (o.renorm) {
     const double S = sum8(w);
     share = S > 0.0 ? w / S : 0.0;
   }
   const double dot = o.score == 0 || o.renorm ? sum8(share * c) : 0.0;
-  const float dz = live ? (float)(share * (c - dot) * (o.score == 0 ? 1.0 : 1.0 - w)) : 0.0f;
+  const float dz = live ? (float)(share * (c - dot) * rest) : 0.0f;
   if (zero) {
     // 4 rows of zeros in one run
     const int rows = min(4, T - t0), n = rows * E;

@@ -117,3 +117,21 @@ def test_gradients_of_masked_and_dropped_slots_are_not_read(kind, renorm, what):
                                               torch.from_numpy(idx).cuda(), score=kind, renorm=renorm)
     want, got = run(np.where(used, dg, np.float32(0))), run(np.where(used, dg, np.float32(what)))
     assert not used.all() and torch.isfinite(want).all() and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+def test_sigmoid_scores_next_to_one(renorm):
+    """p (1 - p) of logits up to 80: exp(-z) of 64 bits, where 1 - p has none left from 37 on."""
+    z = np.array([[20, 30, 35, 36, -3], [37, 40, 50, 60, 1], [38, 70, 45, 80, 90]], np.float32)
+    idx = np.tile([0, 1, 2, 3], (3, 1))
+    dg = np.array([[1, -2, 0.5, 1], [3, 1, -1, 2], [0.25, 2, 1, -1]], np.float32)
+    got = moe.route_scored_backward(torch.from_numpy(dg).cuda(), torch.from_numpy(z).cuda(),
+                                    torch.from_numpy(idx.astype(np.int32)).cuda(), score=1, renorm=renorm).cpu().double().numpy()
+    if renorm:
+        q, s = _shares(z, idx, 1)
+        d = q * (dg - (q * dg).sum(1, keepdims=True)) / (1 + np.exp(s))
+    else:
+        s = z[:, :4].astype(np.float64)
+        d = dg / (1 + np.exp(-s)) / (1 + np.exp(s))
+    # a rounding to fp32; 64-bit ones of the sum of 4 shares, of terms up to 4 |d|
+    assert np.all(np.abs(got[:, :4] - d) <= (ref.F32 + 1e-14) * np.abs(d)) and not got[:, 4].any()
