@@ -16,11 +16,12 @@
 //           order.  For the weight's gradient, whose tiles are few and reductions long.
 //
 // The tensor cores truncate as they add a product to an accumulator, so a sum's error
-// grows with the number of MMAs in its chain.  Outputs in fp32 (PROMO) therefore leave
-// the accumulator every `chunk` k-blocks and are summed on in registers, rounded to
-// nearest; the lower terms of B have accumulator columns of their own, so that they add
-// nothing to the chain of the highest.  bf16 outputs, whose last rounding is far larger,
-// keep one chain.
+// grows with the number of MMAs in its chain: by at most a step, 2^-23, of sum|a b| per MMA.
+// Sums therefore leave the accumulator every `chunk` k-blocks and are summed on in registers,
+// rounded to nearest (PROMO): every CHAIN_F32 for outputs in fp32; the lower terms of B have
+// accumulator columns of their own, so that they add nothing to the chain of the highest.
+// bf16 outputs, whose last rounding is far larger, do it every CHAIN_BF16, and up to that
+// length run in kernels without the sums.
 #include "gemm.cuh"
 
 #include <string.h>
@@ -36,6 +37,8 @@ constexpr int A_BYTES = 16384;            // a CTA's A tile of a k-block: 128 ro
 constexpr int LOW_COLS = 128;             // where an accumulator keeps the lower terms' products
 constexpr int G_RING = 196608;            // bytes of the operand ring
 constexpr int G_STAGING = G_EPI * 4096;   // per epilogue warp: 32 rows x 32 fp32 columns
+constexpr int CHAIN_F32 = 8;              // k-blocks of 4 MMAs: within 32 2^-23 = 2^-18 of sum|a b|
+constexpr int CHAIN_BF16 = 256;           // within 1024 2^-23 = 2^-13: a 32nd of bf16's last rounding
 constexpr double G_FILL = 50.0;           // see cost()
 constexpr uint64_t G_TIMEOUT = 2000000000ull;
 
@@ -430,7 +433,7 @@ __device__ __forceinline__ void join_tiles(const Epilogue& e, uint32_t base, int
   }
 }
 
-template <int PROMO>
+template <bool F32>
 __device__ __forceinline__ Epilogue load_epilogue(const GemmArgs& a, const CUtensorMap& tm_out, const CUtensorMap& tm_pre,
                                                   int lane, uint8_t* st, float* cols) {
   Epilogue e;
@@ -441,7 +444,7 @@ __device__ __forceinline__ Epilogue load_epilogue(const GemmArgs& a, const CUten
   e.tm_out = keep(a.tma_out ? &tm_out : nullptr);
   e.tm_pre = keep(a.tma_pre ? &tm_pre : nullptr);
   e.act = keep(a.ep.act);
-  e.f32 = PROMO != 0;
+  e.f32 = F32;
   e.M = keep(a.M);
   e.N = keep(a.N);
   e.lane = lane;
@@ -456,8 +459,9 @@ __device__ __forceinline__ Epilogue load_epilogue(const GemmArgs& a, const CUten
 __device__ __forceinline__ int chunk_of(int half, int i) { return ((i >> 1) * 2 + half) * 2 + (i & 1); }
 
 // PROMO: chunks per epilogue warp whose sums are kept in registers (2 for BN <= 128: with 4
-// the sums leave too few registers, and the epilogue's own spill), or 0.
-template <int CG, bool AMN, bool BMN, int PROMO>
+// the sums leave too few registers, and the epilogue's own spill), or 0.  F32: the tiles leave
+// in fp32, as outputs or slices.
+template <int CG, bool AMN, bool BMN, int PROMO, bool F32>
 __global__ void __launch_bounds__(G_THREADS, 1)
 gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
             const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ CUtensorMap tm_pre,
@@ -654,7 +658,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
     const int q = warp & 3, half = (warp - 2) >> 2;   // TMEM lanes 32 q ..
     int acc = 0;
     uint32_t aph = 0;
-    Epilogue ep = load_epilogue<PROMO>(a, tm_out, tm_pre, lane, staging + (warp - 2) * 4096, ctl->bias[warp - 2]);
+    Epilogue ep = load_epilogue<F32>(a, tm_out, tm_pre, lane, staging + (warp - 2) * 4096, ctl->bias[warp - 2]);
     const int BN = keep(a.BN);
     const bool low = a.PB > 1;
     bool ok = true;
@@ -777,7 +781,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
     if (!*reinterpret_cast<volatile uint32_t*>(&ctl->abort)) {
       int tm, tn;
       tile_at(a, t0, &tm, &tn);
-      const Epilogue ep = load_epilogue<PROMO>(a, tm_out, tm_pre, lane, staging, nullptr);
+      const Epilogue ep = load_epilogue<F32>(a, tm_out, tm_pre, lane, staging, nullptr);
       const int row = split * (128 / S), m0 = tm * (128 * CG) + rank * 128 + row, n0 = tn * a.BN;
       if (S == 2) join_tiles<2, 4>(ep, smem_u32(smem), a.BN, m0, n0, row, CG, rank);
       else if (S == 4) join_tiles<4, 2>(ep, smem_u32(smem), a.BN, m0, n0, row, CG, rank);
@@ -846,12 +850,12 @@ bool encode_out(CUtensorMap* m, void* p, int M, int N, int ld, int slices, int f
             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int CG, bool AMN, bool BMN, int PROMO>
+template <int CG, bool AMN, bool BMN, int PROMO, bool F32>
 cudaError_t run(const CUtensorMap (&m)[4], const GemmArgs& a, int grid, int dev, cudaStream_t s) {
   static bool configured[64] = {false};
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!configured[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(gemm_kernel<CG, AMN, BMN, PROMO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(gemm_kernel<CG, AMN, BMN, PROMO, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)G_SMEM);
     if (e != cudaSuccess) return e;
     configured[dev] = true;
@@ -870,16 +874,23 @@ cudaError_t run(const CUtensorMap (&m)[4], const GemmArgs& a, int grid, int dev,
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG * a.S > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, gemm_kernel<CG, AMN, BMN, PROMO>, m[0], m[1], m[2], m[3], a);
+  return cudaLaunchKernelEx(&cfg, gemm_kernel<CG, AMN, BMN, PROMO, F32>, m[0], m[1], m[2], m[3], a);
 }
 
-template <int CG, int PROMO>
+template <int CG, int PROMO, bool F32>
 cudaError_t run_major(const GemmProblem& p, const CUtensorMap (&m)[4], const GemmArgs& a, int grid, int dev,
                       cudaStream_t s) {
-  if (p.a_mn) return p.b_mn ? run<CG, true, true, PROMO>(m, a, grid, dev, s) : cudaErrorInvalidValue;
-  if (p.b_mn) return run<CG, false, true, PROMO>(m, a, grid, dev, s);
-  if constexpr (PROMO != 0) return cudaErrorInvalidValue;   // no product of the layer has an fp32 output here
-  else return run<CG, false, false, 0>(m, a, grid, dev, s);
+  if (p.a_mn) return p.b_mn ? run<CG, true, true, PROMO, F32>(m, a, grid, dev, s) : cudaErrorInvalidValue;
+  if (p.b_mn) return run<CG, false, true, PROMO, F32>(m, a, grid, dev, s);
+  if constexpr (F32) return cudaErrorInvalidValue;          // no product of the layer has an fp32 output here
+  else return run<CG, false, false, PROMO, false>(m, a, grid, dev, s);
+}
+
+template <int CG>
+cudaError_t run_sums(const GemmProblem& p, const CUtensorMap (&m)[4], const GemmArgs& a, bool f32, bool promo, int grid,
+                     int dev, cudaStream_t s) {
+  if (f32) return a.BN <= 128 ? run_major<CG, 2, true>(p, m, a, grid, dev, s) : run_major<CG, 4, true>(p, m, a, grid, dev, s);
+  return promo ? run_major<CG, 4, false>(p, m, a, grid, dev, s) : run_major<CG, 0, false>(p, m, a, grid, dev, s);
 }
 
 // SM cycles of one tile configuration, from rates measured on one B200: an MMA of
@@ -905,7 +916,7 @@ int clusters_of(int dev, int nsm, int size) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int n = 0;
-    auto kernel = gemm_kernel<2, false, true, 0>;
+    auto kernel = gemm_kernel<2, false, true, 0, false>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G_SMEM) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
       cudaGetLastError();
@@ -1063,9 +1074,9 @@ cudaError_t launch_gemm(const GemmProblem& p, cudaStream_t s) {
   a.b_whole = p.b_mn ? p.N % 64 == 0 && cols % 64 == 0 : p.K % 64 == 0;
   a.nst = min(G_MAX_NST, G_RING / a.stage_bytes);
   a.group = c.CG == 2 ? 8 : 16;
-  // 32 MMAs in a chain keep an fp32 output within 1e-6 of the exact sum
-  const bool promo = p.ep.out_f32 || a.SW > 1;
-  a.chunk = p.ep.out_f32 ? 8 : 1 << 30;
+  const bool f32 = p.ep.out_f32 || a.SW > 1;
+  a.chunk = p.ep.out_f32 ? CHAIN_F32 : CHAIN_BF16;
+  const bool promo = cdiv(cdiv(p.K, 64), a.S * a.SW) > a.chunk;
   CUtensorMap m[4];
   if (!(p.a_mn ? encode4(&m[0], p.A, p.M, p.K, 64 * a.kps, a.a_whole, 2, 1)
                : encode4(&m[0], p.A, p.K, p.M, 128, a.a_whole, a.kps, 1)) ||
@@ -1084,12 +1095,7 @@ cudaError_t launch_gemm(const GemmProblem& p, cudaStream_t s) {
   }
   if (a.tma_pre && !encode_out(&m[3], p.ep.pre, p.M, p.N, p.N, 1, 0)) return cudaErrorInvalidValue;
   const int grid = c.CG * (a.S > 1 ? ntiles * a.S : min(ntiles * a.SW, clusters_of(dev, nsm, c.CG)));
-  if (c.CG == 2)
-    e = !promo ? run_major<2, 0>(p, m, a, grid, dev, s)
-        : a.BN <= 128 ? run_major<2, 2>(p, m, a, grid, dev, s) : run_major<2, 4>(p, m, a, grid, dev, s);
-  else
-    e = !promo ? run_major<1, 0>(p, m, a, grid, dev, s)
-        : a.BN <= 128 ? run_major<1, 2>(p, m, a, grid, dev, s) : run_major<1, 4>(p, m, a, grid, dev, s);
+  e = c.CG == 2 ? run_sums<2>(p, m, a, f32, promo, grid, dev, s) : run_sums<1>(p, m, a, f32, promo, grid, dev, s);
   if (e != cudaSuccess || a.SW == 1) return e;
   const long vecs = (long)p.M * ld4;
   const int blocks = (int)(vecs < 16L * nsm * 256 ? (vecs + 255) / 256 : 16L * nsm);

@@ -322,8 +322,11 @@ moe_status moe_combine_backward(const void* dout, const void* y, const int32_t* 
  * accumulated in fp32 and rounded once.  Any M, K, N from 1 to 2^30 (rows that are no
  * 16-byte multiples are first copied into padded ones in the workspace, unless there are
  * few); sums run in an order that depends on the shape and the device alone, so equal
- * calls give equal bits.  Sums of an fp32 output keep 32 bits however long they are (the
- * tensor cores' own accumulators truncate: they hold no more than 512 products of it). */
+ * calls give equal bits.  The tensor cores' own accumulators truncate, so they hold 512
+ * products of an fp32 output's sum at the most, and 16384 of a bf16 output's, and what they
+ * held is added in fp32, rounded to nearest: before its rounding to the output's type a sum
+ * is within 2^-18 (fp32 outputs) or 2^-13 (bf16) of sum |x w|, and 2^-24 more for each such
+ * run of products. */
 typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 /* erf */ } moe_act;
 typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 } moe_dtype;
 
