@@ -325,13 +325,13 @@ __device__ __forceinline__ void finish_chunk(Epilogue& e, uint32_t tacc, float b
   if (e.pre) emit16(e, v, e.tm_pre, e.pre, row0, col, cend);
   if (e.act == 1) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = act_f32(1, v[i]);
+    for (int i = 0; i < 32; ++i) v[i] = act_f32(1, v[i], e.f32);
   } else if (e.act == 2) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = act_f32(2, v[i]);
+    for (int i = 0; i < 32; ++i) v[i] = act_f32(2, v[i], e.f32);
   } else if (e.act == 3) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = act_f32(3, v[i]);
+    for (int i = 0; i < 32; ++i) v[i] = act_f32(3, v[i], e.f32);
   }
   if (e.residual) {
 #pragma unroll
@@ -362,7 +362,7 @@ __device__ __forceinline__ void finish4(const Epilogue& e, int m, int n, float4 
   }
   if (e.act) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = act_f32(e.act, u[i]);
+    for (int i = 0; i < 4; ++i) u[i] = act_f32(e.act, u[i], e.f32);
   }
   if (e.f32) {
     float* o = static_cast<float*>(e.out) + at;

@@ -13,14 +13,23 @@ namespace moe {
 
 namespace {
 
+// EXACT: for a du that is kept in more than bf16.
+template <bool EXACT>
 __device__ __forceinline__ float dact_f32(int act, float u) {
   switch (act) {
     case 1: return u > 0.0f ? 1.0f : 0.0f;
     case 2: {
+      if (EXACT) {
+        const Sigmoid s = sigmoid_f32(u);
+        return s.p * (1.0f + u * s.q);
+      }
       const float p = __fdividef(1.0f, 1.0f + __expf(-u));
       return p * (1.0f + u * (1.0f - p));
     }
-    case 3: return 0.5f * (1.0f + erff(u * 0.70710678f)) + u * __expf(-0.5f * u * u) * 0.39894228f;
+    case 3: {
+      const Normal g = normal_f32<EXACT>(u);
+      return g.P + u * g.e * 0.39894228f;
+    }
   }
   return 1.0f;
 }
@@ -90,7 +99,7 @@ size_t pack_bytes(long rows, int n) { return n % 8 ? up256((size_t)rows * pad8(n
 constexpr int DACT_R = 2;
 enum { DACT_BF16, DACT_F32, DACT_ANY };
 
-template <int ACT, int MODE>
+template <int ACT, int MODE, bool EXACT>
 __global__ void __launch_bounds__(256, 4) dact_kernel(const void* __restrict__ dout, int f32,
                                                    const __nv_bfloat16* __restrict__ pre, int M,
                                                    int N, int rows, int planes, __nv_bfloat16* __restrict__ du,
@@ -144,7 +153,7 @@ __global__ void __launch_bounds__(256, 4) dact_kernel(const void* __restrict__ d
         if (m >= m1) break;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if (ACT) v[r][i] *= dact_f32(ACT, u[r][i]);
+          if (ACT) v[r][i] *= dact_f32<EXACT>(ACT, u[r][i]);
           sum[i] += v[r][i];
         }
         __nv_bfloat16* to = du + (size_t)m * planes * n8 + n;
@@ -178,10 +187,11 @@ __global__ void __launch_bounds__(256, 4) dact_kernel(const void* __restrict__ d
   }
 }
 
-template <int ACT>
+template <int ACT, bool EXACT>
 cudaError_t launch_dact(const LinearBwdArgs& a, int rows, int planes, __nv_bfloat16* du, int n8, float* part,
                         cudaStream_t s) {
-  auto kernel = a.N % 8 ? dact_kernel<ACT, DACT_ANY> : a.dout_f32 ? dact_kernel<ACT, DACT_F32> : dact_kernel<ACT, DACT_BF16>;
+  auto kernel = a.N % 8 ? dact_kernel<ACT, DACT_ANY, EXACT>
+                : a.dout_f32 ? dact_kernel<ACT, DACT_F32, EXACT> : dact_kernel<ACT, DACT_BF16, EXACT>;
   return launch_pdl(kernel, dim3(cdiv(n8, 128), cdiv(a.M, rows)), dim3(256), 0, s, a.dout, a.dout_f32,
                     static_cast<const __nv_bfloat16*>(a.pre), a.M, a.N, rows, planes, du, n8, part);
 }
@@ -263,8 +273,14 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, void* ws, cudaStream_t s) 
     float* sums = !a.dbias ? nullptr : nblk == 1 ? a.dbias : part;
     __nv_bfloat16* to = (__nv_bfloat16*)du.p;
     const int n = direct ? 0 : terms;
-    e = a.act == 1 ? launch_dact<1>(a, rows, n, to, n8, sums, s) : a.act == 2 ? launch_dact<2>(a, rows, n, to, n8, sums, s)
-        : a.act == 3 ? launch_dact<3>(a, rows, n, to, n8, sums, s) : launch_dact<0>(a, rows, n, to, n8, sums, s);
+    switch (a.act * 2 + (terms > 1)) {
+      case 0: case 1: e = launch_dact<0, false>(a, rows, n, to, n8, sums, s); break;
+      case 2: case 3: e = launch_dact<1, false>(a, rows, n, to, n8, sums, s); break;
+      case 4: e = launch_dact<2, false>(a, rows, n, to, n8, sums, s); break;
+      case 5: e = launch_dact<2, true>(a, rows, n, to, n8, sums, s); break;
+      case 6: e = launch_dact<3, false>(a, rows, n, to, n8, sums, s); break;
+      default: e = launch_dact<3, true>(a, rows, n, to, n8, sums, s); break;
+    }
     if (e != cudaSuccess) return e;
   }
   if (direct) du = {a.dout, (size_t)n8 * 2, 0, 1};

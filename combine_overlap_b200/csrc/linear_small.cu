@@ -48,7 +48,7 @@ __device__ __forceinline__ void finish1(const LinearEpi& e, int N, int m, int n,
   const size_t at = (size_t)m * N + n;
   if (e.bias) v += __ldg(e.bias + n);
   if (e.pre) static_cast<__nv_bfloat16*>(e.pre)[at] = __float2bfloat16(v);
-  v = act_f32(e.act, v);
+  v = act_f32(e.act, v, e.out_f32);
   if (e.out_f32) {
     if (e.residual) v += static_cast<const float*>(e.residual)[at];
     static_cast<float*>(e.out)[at] = v;
