@@ -201,6 +201,11 @@ int choose_variant(int T, int f, int E, int k, unsigned flags) {
 inline int bands_per_tile(int V) { return V == 1 ? 1 : 2; }
 inline int ctas_per_tile(int V) { return V == 2 ? 2 : 1; }
 
+// A product's status: a forced shape that it cannot take is no CUDA error.
+inline moe_status linear_status(cudaError_t e) {
+  return e == cudaErrorNotSupported ? MOE_ERR_UNSUPPORTED : cuda_status(e);
+}
+
 inline bool ok_dtype(int t) { return t == MOE_DTYPE_BF16 || t == MOE_DTYPE_F32; }
 
 // Sizes of a linear layer: any M, K, N whose matrices stay under 2^40 elements.
@@ -563,7 +568,7 @@ moe_status moe_linear(const moe_linear_args* args, void* ws, size_t ws_bytes, vo
   const size_t need = linear_ws_bytes(A.M, A.K, A.N);
   if (need && (!ws || !aligned16(ws) || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   LinearArgs a = {A.M, A.K, A.N, A.x, A.W, {A.bias, A.residual, A.act, A.out_dtype, A.out, A.pre}};
-  return cuda_status(launch_linear(a, ws, static_cast<cudaStream_t>(stream)));
+  return linear_status(launch_linear(a, ws, static_cast<cudaStream_t>(stream)));
 }
 
 moe_status moe_linear_backward(const moe_linear_bwd_args* args, void* ws, size_t ws_bytes, void* stream) {
@@ -582,7 +587,14 @@ moe_status moe_linear_backward(const moe_linear_bwd_args* args, void* ws, size_t
   if (!ws || !aligned16(ws) || ws_bytes < need) return MOE_ERR_WORKSPACE;
   LinearBwdArgs a = {A.M, A.K, A.N, A.dout, A.x, A.W, A.act ? A.pre : nullptr, A.act, A.dout_dtype,
                      A.dW_dtype, A.dx, A.dW, A.dbias};
-  return cuda_status(launch_linear_bwd(a, ws, static_cast<cudaStream_t>(stream)));
+  return linear_status(launch_linear_bwd(a, ws, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_linear_debug_set(const moe_linear_debug* d) {
+  if (d && (d->cg < 0 || (d->cg > 0 && (d->bn < 1 || d->s < 1 || d->sw < 1)))) return MOE_ERR_INVALID;
+  if (d && d->cg > 0) linear_debug(d->cg, d->bn, d->s, d->sw);
+  else linear_debug(0, 0, 0, 0);
+  return MOE_OK;
 }
 
 moe_status moe_linear_get_status(void* stream) {

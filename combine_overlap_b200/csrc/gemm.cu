@@ -974,6 +974,18 @@ Shape pick(const GemmProblem& p, int dev, int nsm) {
   return best;
 }
 
+// Whether a shape given by gemm_debug is one that pick() may come to for some size.
+bool legal(const GemmProblem& p, int dev, int nsm, Shape c) {
+  const int nkb = cdiv(p.K, 64), slices = p.ws ? gemm_slices(p.M, p.N) : 1;
+  if (c.CG < 1 || c.CG > 2 || (c.CG == 2 && p.M <= 128)) return false;
+  if (c.BN != 16 && (c.BN < 32 || c.BN % 32 != 0 || c.BN > min(p.B.planes > 1 ? 128 : 256, cdiv(p.N, 32) * 32))) return false;
+  if (c.BN == 16 && (c.CG == 2 || p.N > 16)) return false;
+  if (c.S < 1 || c.SW < 1 || (c.S & (c.S - 1)) != 0 || c.S * c.CG > 8 || (c.S > 1 && c.SW > 1)) return false;
+  if (c.SW > 1 && (c.SW > slices || c.SW > nkb / 4)) return false;
+  const int tiles = cdiv(p.M, 128 * c.CG) * cdiv(p.N, c.BN);
+  return c.S == 1 || (nkb >= 4 * c.S && tiles <= clusters_of(dev, nsm, c.S * c.CG));
+}
+
 // out = the sum of the slices, in order: one thread per 4 columns.  The first blocks take
 // the column sums.
 template <int U>
@@ -1019,6 +1031,9 @@ __global__ void __launch_bounds__(256) join_kernel(const float4* __restrict__ ws
 
 }  // namespace
 
+// What moe_linear_debug_set has set for the calling thread's products; CG = 0: nothing.
+thread_local Shape gemm_debug = {0, 0, 0, 0};
+
 // Slices for which the workspace has room: up to 16, and no more than 40 MB of them (two
 // waves of 256 x 256 tiles).
 int gemm_slices(int M, int N) {
@@ -1057,7 +1072,9 @@ cudaError_t launch_gemm(const GemmProblem& p, cudaStream_t s) {
   a.M = p.M; a.N = p.N; a.K = p.K;
   a.PB = p.B.planes;
   a.ep = p.ep;
-  const Shape c = pick(p, dev, nsm);
+  Shape c = gemm_debug;
+  if (c.CG == 0) c = pick(p, dev, nsm);
+  else if (!legal(p, dev, nsm, c)) return cudaErrorNotSupported;
   a.BN = c.BN;
   a.S = c.S;
   a.SW = c.SW;
@@ -1107,6 +1124,8 @@ cudaError_t launch_gemm(const GemmProblem& p, cudaStream_t s) {
   return launch_pdl(join_kernel<4>, dim3(blocks + (sums.out ? cdiv(sums.N, 32) : 0)), dim3(256), 0, s,
                     static_cast<const float4*>(p.ws), a.SW, p.M, p.N, ld4, p.ep.out, p.ep.out_f32, sums);
 }
+
+void linear_debug(int CG, int BN, int S, int SW) { gemm_debug = {CG, BN, S, SW}; }
 
 cudaError_t linear_timeout(cudaStream_t s, uint32_t* word) {
   cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_linear_timeout, 4, 0, cudaMemcpyDeviceToHost, s);

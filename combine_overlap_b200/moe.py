@@ -7,6 +7,7 @@ built this module raises at import -- there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -117,6 +118,10 @@ class LinearBwdArgs(ctypes.Structure):
     ]
 
 
+class LinearDebug(ctypes.Structure):
+    _fields_ = [("cg", ctypes.c_int), ("bn", ctypes.c_int), ("s", ctypes.c_int), ("sw", ctypes.c_int)]
+
+
 _P, _I, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 _lib.moe_workspace_size.argtypes = [_I, _I, _I, _I, _I]
 _lib.moe_workspace_size.restype = _S
@@ -161,6 +166,8 @@ _lib.moe_linear_backward_workspace_size.argtypes = [_I, _I, _I]
 _lib.moe_linear_backward_workspace_size.restype = _S
 _lib.moe_linear.argtypes = [_P, _P, _S, _P]
 _lib.moe_linear_backward.argtypes = [_P, _P, _S, _P]
+_lib.moe_linear_debug_set.argtypes = [_P]
+_lib.moe_linear_debug_set.restype = _I
 _lib.moe_linear_get_status.argtypes = [_P]
 _lib.moe_linear_get_status.restype = _I
 for _fn in ("moe_route_scored", "moe_route_scored_backward", "moe_layer_forward_scored",
@@ -595,6 +602,19 @@ def linear_backward(dout, x, W, pre=None, act=ACT_NONE, dW_dtype=torch.float32, 
     if r:
         _check(r, "moe_linear_backward")
     return dx, dW, db
+
+
+@contextlib.contextmanager
+def linear_debug(cg=0, bn=0, s=1, sw=1):
+    """Within it, this thread's tensor-core products run with the given tile and splits
+    (moe_linear_debug_set; cg = 0: the library's choice); MOE_ERR_UNSUPPORTED where a
+    product of that size is never cut that way."""
+    d = LinearDebug(cg, bn, s, sw)
+    _check(_lib.moe_linear_debug_set(ctypes.byref(d)), "moe_linear_debug_set")
+    try:
+        yield
+    finally:
+        _lib.moe_linear_debug_set(None)
 
 
 def linear_get_status(stream=None) -> int:

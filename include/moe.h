@@ -372,6 +372,19 @@ size_t moe_linear_backward_workspace_size(int M, int K, int N);
 moe_status moe_linear_backward(const moe_linear_bwd_args* args, void* ws, size_t ws_bytes,
                                void* stream);
 
+/* Debug aid, for the calling thread's tensor-core products from here on (NULL: back to the
+ * library's choice): the tile and the splits of the reduction, whatever their cost.
+ * MOE_ERR_UNSUPPORTED from moe_linear or moe_linear_backward: a product of that size is
+ * never cut that way (a pair for M <= 128, tiles wider than N, splits of fewer than 4
+ * 64-element blocks, clusters that do not all fit, slices without room for them). */
+typedef struct {
+  int cg;                   /* 1: 128-row tiles, 2: 256-row tiles of CTA pairs; 0: chosen */
+  int bn;                   /* columns per tile: 16 (N <= 16), 32, 64, .. 256        */
+  int s;                    /* the reduction over a cluster of s tiles: 1, 2, 4, 8   */
+  int sw;                   /* the reduction in sw slices (dW): 1 .. 16              */
+} moe_linear_debug;
+moe_status moe_linear_debug_set(const moe_linear_debug* d);
+
 /* Synchronises `stream`, then tells whether a bounded wait (2 s) of any moe_linear or
  * moe_linear_backward on the current device ran out since the last call of this
  * (MOE_ERR_TIMEOUT: those outputs are not to be used), and clears the note. */
