@@ -1067,6 +1067,14 @@ cudaError_t launch_gemm(const GemmProblem& p, cudaStream_t s) {
   int dev = 0, nsm = 0;
   cudaError_t e = device_of(&dev, &nsm);
   if (e != cudaSuccess) return e;
+  // Encoding a tensor map takes a current context, which a thread that has launched nothing
+  // yet does not have: setting its device makes that device's context current.
+  static thread_local int bound = -1;
+  if (bound != dev) {
+    e = cudaSetDevice(dev);
+    if (e != cudaSuccess) return e;
+    bound = dev;
+  }
   GemmArgs a;
   memset(&a, 0, sizeof(a));
   a.M = p.M; a.N = p.N; a.K = p.K;
