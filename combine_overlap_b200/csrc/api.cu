@@ -591,16 +591,22 @@ moe_status moe_linear_backward(const moe_linear_bwd_args* args, void* ws, size_t
 }
 
 moe_status moe_linear_debug_set(const moe_linear_debug* d) {
-  if (d && (d->cg < 0 || (d->cg > 0 && (d->bn < 1 || d->s < 1 || d->sw < 1)))) return MOE_ERR_INVALID;
-  if (d && d->cg > 0) linear_debug(d->cg, d->bn, d->s, d->sw);
-  else linear_debug(0, 0, 0, 0);
+  const moe_linear_debug none = {};
+  const moe_linear_debug& q = d ? *d : none;
+  if (q.cg < 0 || (q.cg > 0 && (q.bn < 1 || q.s < 1 || q.sw < 1)) || q.timeout_us < 0) return MOE_ERR_INVALID;
+  linear_debug(q.cg, q.bn, q.s, q.sw, q.timeout_us, q.withhold);
   return MOE_OK;
 }
 
 moe_status moe_linear_get_status(void* stream) {
-  uint32_t word = 0;
-  MOE_TRY(linear_timeout(static_cast<cudaStream_t>(stream), &word));
-  return word ? MOE_ERR_TIMEOUT : MOE_OK;
+  static uint32_t seen[64] = {};
+  uint32_t count = 0;
+  int dev = 0;
+  MOE_TRY(cudaGetDevice(&dev));
+  MOE_TRY(linear_timeouts(static_cast<cudaStream_t>(stream), &count));
+  if (dev < 0 || dev >= 64 || count == seen[dev]) return MOE_OK;
+  seen[dev] = count;
+  return MOE_ERR_TIMEOUT;
 }
 
 size_t moe_ep_owner_workspace_size(int N, int d, int f, int El, int W) {

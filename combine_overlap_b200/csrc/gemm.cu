@@ -40,7 +40,7 @@ constexpr int G_STAGING = G_EPI * 4096;   // per epilogue warp: 32 rows x 32 fp3
 constexpr int CHAIN_F32 = 8;              // k-blocks of 4 MMAs: within 32 2^-23 = 2^-18 of sum|a b|
 constexpr int CHAIN_BF16 = 256;           // within 1024 2^-23 = 2^-13: a 32nd of bf16's last rounding
 constexpr double G_FILL = 50.0;           // see cost()
-constexpr uint64_t G_TIMEOUT = 2000000000ull;
+constexpr uint64_t G_TIMEOUT = 2000000000ull;   // ns; moe_linear_debug_set may set another
 
 struct GemmCtl {
   uint64_t full[G_MAX_NST], empty[G_MAX_NST];   // full: counted on the pair's leader
@@ -48,15 +48,15 @@ struct GemmCtl {
   uint64_t mma_done;
   uint32_t tmem_base;
   uint32_t abort;                         // a bounded wait of this CTA ran out
+  uint64_t limit;                         // ns that a wait may take
   alignas(16) float bias[G_EPI][32];                  // of each epilogue warp's chunk
 };
 
 constexpr size_t G_SMEM = 1024 + (size_t)G_RING + G_STAGING + sizeof(GemmCtl);
 static_assert(G_SMEM <= 227 * 1024, "over the 227 KB per-CTA limit");
 
-// Set when a bounded wait of a product ran out; read and cleared by
-// moe_linear_get_status.
-__device__ uint32_t g_linear_timeout;
+// How many CTAs of products have given up a bounded wait so far.
+__device__ uint32_t g_linear_timeouts;
 
 struct GemmArgs {
   int M, N, K;
@@ -72,6 +72,8 @@ struct GemmArgs {
   int chunk;                              // k-blocks per accumulator chain, a multiple of kps
   int group;                              // row tiles per raster group
   int tma_out, tma_pre;                   // rows of 16-byte multiples: chunks leave by TMA
+  int withhold;                           // debug: block 0 brings no operands
+  uint64_t limit;                         // ns that a wait may take
   LinearEpi ep;
 };
 
@@ -100,9 +102,9 @@ __device__ __forceinline__ bool g_wait(uint64_t* bar, uint32_t parity, GemmCtl* 
     if (__all_sync(0xffffffffu, ready)) return true;
     if ((++n & 1023u) != 0) continue;
     const uint64_t now = globaltimer();
-    if (deadline == 0) deadline = now + G_TIMEOUT;
+    if (deadline == 0) deadline = now + *const_cast<volatile uint64_t*>(&ctl->limit);
     if (__any_sync(0xffffffffu, *ab != 0 || now > deadline)) {
-      if (atomicExch(const_cast<uint32_t*>(ab), 1u) == 0) atomicExch(&g_linear_timeout, 1u);
+      if (atomicExch(const_cast<uint32_t*>(ab), 1u) == 0) atomicAdd(&g_linear_timeouts, 1u);
       return false;
     }
   }
@@ -483,6 +485,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
     for (int i = 0; i < 2; ++i) { mbar_init(&ctl->tfull[i], 1); mbar_init(&ctl->tempty[i], G_EPI * CG); }
     mbar_init(&ctl->mma_done, 1);
     ctl->abort = 0;
+    ctl->limit = a.limit;
     mbar_fence_init();
     fence_proxy_async_shared();
     tma_prefetch_desc(&tm_a);
@@ -516,7 +519,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
   if (warp == 0) {
     int stage = 0;
     uint32_t ph = 0;
-    bool ok = true;
+    bool ok = !(a.withhold && blockIdx.x == 0);
     const int kps = keep(a.kps), nst = keep(a.nst), PB = keep(a.PB), boxes = keep(a.b_boxes);
     const int b_bytes = keep(a.b_bytes), stage_bytes = keep(a.stage_bytes);
     const int a_whole = keep(a.a_whole), b_whole = keep(a.b_whole);
@@ -569,7 +572,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
     if (!ok) {
       // copies may still be landing: a bounded wait until every stage's are in (a pair's
       // second CTA, whose copies are counted on the leader, waits a fixed time)
-      const uint64_t until = globaltimer() + (rank == 0 ? G_TIMEOUT : 1000000ull);
+      const uint64_t until = globaltimer() + (rank == 0 ? a.limit : 1000000ull);
       for (int i = 0; i < a.nst; ++i)
         for (uint32_t par = 0; par < 2; ++par)
           while ((rank || !mbar_try_wait(&ctl->full[i], par)) && globaltimer() < until) {}
@@ -1031,8 +1034,13 @@ __global__ void __launch_bounds__(256) join_kernel(const float4* __restrict__ ws
 
 }  // namespace
 
-// What moe_linear_debug_set has set for the calling thread's products; CG = 0: nothing.
-thread_local Shape gemm_debug = {0, 0, 0, 0};
+// What moe_linear_debug_set has set for the calling thread's products.
+struct GemmDebug {
+  Shape shape;                            // CG = 0: chosen by cost
+  uint64_t limit;
+  int withhold;
+};
+thread_local GemmDebug gemm_debug = {{0, 0, 0, 0}, G_TIMEOUT, 0};
 
 // Slices for which the workspace has room: up to 16, and no more than 40 MB of them (two
 // waves of 256 x 256 tiles).
@@ -1080,7 +1088,9 @@ cudaError_t launch_gemm(const GemmProblem& p, cudaStream_t s) {
   a.M = p.M; a.N = p.N; a.K = p.K;
   a.PB = p.B.planes;
   a.ep = p.ep;
-  Shape c = gemm_debug;
+  a.limit = gemm_debug.limit;
+  a.withhold = gemm_debug.withhold;
+  Shape c = gemm_debug.shape;
   if (c.CG == 0) c = pick(p, dev, nsm);
   else if (!legal(p, dev, nsm, c)) return cudaErrorNotSupported;
   a.BN = c.BN;
@@ -1133,14 +1143,12 @@ cudaError_t launch_gemm(const GemmProblem& p, cudaStream_t s) {
                     static_cast<const float4*>(p.ws), a.SW, p.M, p.N, ld4, p.ep.out, p.ep.out_f32, sums);
 }
 
-void linear_debug(int CG, int BN, int S, int SW) { gemm_debug = {CG, BN, S, SW}; }
+void linear_debug(int CG, int BN, int S, int SW, int timeout_us, int withhold) {
+  gemm_debug = {{CG, BN, S, SW}, timeout_us > 0 ? timeout_us * 1000ull : G_TIMEOUT, withhold};
+}
 
-cudaError_t linear_timeout(cudaStream_t s, uint32_t* word) {
-  cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_linear_timeout, 4, 0, cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e != cudaSuccess || *word == 0) return e;
-  const uint32_t zero = 0;
-  e = cudaMemcpyToSymbolAsync(g_linear_timeout, &zero, 4, 0, cudaMemcpyHostToDevice, s);
+cudaError_t linear_timeouts(cudaStream_t s, uint32_t* count) {
+  const cudaError_t e = cudaMemcpyFromSymbolAsync(count, g_linear_timeouts, 4, 0, cudaMemcpyDeviceToHost, s);
   return e == cudaSuccess ? cudaStreamSynchronize(s) : e;
 }
 

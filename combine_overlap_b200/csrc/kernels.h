@@ -163,9 +163,9 @@ cudaError_t launch_linear(const LinearArgs& a, void* ws, cudaStream_t s);
 cudaError_t launch_linear_small(const LinearArgs& a, int num_sms, cudaStream_t s);   // linear_small.cu: few rows
 cudaError_t launch_linear_bwd(const LinearBwdArgs& a, void* ws, cudaStream_t s);
 // gemm.cu: for moe_linear_debug_set
-void linear_debug(int CG, int BN, int S, int SW);
-// gemm.cu: synchronises s; *word = 1 if a wait of a product ran out since the last call.
-cudaError_t linear_timeout(cudaStream_t s, uint32_t* word);
+void linear_debug(int CG, int BN, int S, int SW, int timeout_us, int withhold);
+// gemm.cu: synchronises s; how many CTAs of products have given up a wait on this device so far.
+cudaError_t linear_timeouts(cudaStream_t s, uint32_t* count);
 
 size_t ffn_smem_bytes();
 // CTAs the persistent kernel runs with for tile variant V; also sets the

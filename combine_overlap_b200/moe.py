@@ -12,6 +12,7 @@ import ctypes
 import os
 import re
 import struct
+import threading
 
 import torch
 
@@ -119,7 +120,8 @@ class LinearBwdArgs(ctypes.Structure):
 
 
 class LinearDebug(ctypes.Structure):
-    _fields_ = [("cg", ctypes.c_int), ("bn", ctypes.c_int), ("s", ctypes.c_int), ("sw", ctypes.c_int)]
+    _fields_ = [("cg", ctypes.c_int), ("bn", ctypes.c_int), ("s", ctypes.c_int), ("sw", ctypes.c_int),
+                ("timeout_us", ctypes.c_int), ("withhold", ctypes.c_int)]
 
 
 _P, _I, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
@@ -604,17 +606,23 @@ def linear_backward(dout, x, W, pre=None, act=ACT_NONE, dW_dtype=torch.float32, 
     return dx, dW, db
 
 
+_thread = threading.local()
+
+
 @contextlib.contextmanager
-def linear_debug(cg=0, bn=0, s=1, sw=1):
+def linear_debug(cg=0, bn=0, s=1, sw=1, timeout_us=0, withhold=False):
     """Within it, this thread's tensor-core products run with the given tile and splits
     (moe_linear_debug_set; cg = 0: the library's choice); MOE_ERR_UNSUPPORTED where a
-    product of that size is never cut that way."""
-    d = LinearDebug(cg, bn, s, sw)
+    product of that size is never cut that way.  timeout_us bounds their device waits
+    (0: 2 s); withhold makes those of the first tile run out."""
+    d, before = LinearDebug(cg, bn, s, sw, timeout_us, int(withhold)), getattr(_thread, "linear_debug", None)
     _check(_lib.moe_linear_debug_set(ctypes.byref(d)), "moe_linear_debug_set")
+    _thread.linear_debug = d
     try:
         yield
     finally:
-        _lib.moe_linear_debug_set(None)
+        _thread.linear_debug = before
+        _lib.moe_linear_debug_set(None if before is None else ctypes.byref(before))
 
 
 def linear_get_status(stream=None) -> int:

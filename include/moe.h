@@ -382,12 +382,15 @@ typedef struct {
   int bn;                   /* columns per tile: 16 (N <= 16), 32, 64, .. 256        */
   int s;                    /* the reduction over a cluster of s tiles: 1, 2, 4, 8   */
   int sw;                   /* the reduction in sw slices (dW): 1 .. 16              */
+  int timeout_us;           /* the bound of a device wait; 0: 2 s                    */
+  int withhold;             /* 1: the first tile's operands never come, so that waits
+                               run out (MOE_ERR_TIMEOUT of moe_linear_get_status)    */
 } moe_linear_debug;
 moe_status moe_linear_debug_set(const moe_linear_debug* d);
 
 /* Synchronises `stream`, then tells whether a bounded wait (2 s) of any moe_linear or
  * moe_linear_backward on the current device ran out since the last call of this
- * (MOE_ERR_TIMEOUT: those outputs are not to be used), and clears the note. */
+ * (MOE_ERR_TIMEOUT: those outputs are not to be used). */
 moe_status moe_linear_get_status(void* stream);
 
 /* ---- Expert parallelism: the fused return ---------------------------------
