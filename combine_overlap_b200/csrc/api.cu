@@ -598,8 +598,13 @@ moe_status moe_linear_debug_set(const moe_linear_debug* d) {
   return MOE_OK;
 }
 
+moe_status moe_linear_timeouts(void* stream, uint32_t* count) {
+  if (!count) return MOE_ERR_INVALID;
+  return cuda_status(linear_timeouts(static_cast<cudaStream_t>(stream), count));
+}
+
 moe_status moe_linear_get_status(void* stream) {
-  static uint32_t seen[64] = {};
+  static thread_local uint32_t seen[64] = {};
   uint32_t count = 0;
   int dev = 0;
   MOE_TRY(cudaGetDevice(&dev));

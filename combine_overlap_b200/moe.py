@@ -170,6 +170,8 @@ _lib.moe_linear.argtypes = [_P, _P, _S, _P]
 _lib.moe_linear_backward.argtypes = [_P, _P, _S, _P]
 _lib.moe_linear_debug_set.argtypes = [_P]
 _lib.moe_linear_debug_set.restype = _I
+_lib.moe_linear_timeouts.argtypes = [_P, ctypes.POINTER(ctypes.c_uint32)]
+_lib.moe_linear_timeouts.restype = _I
 _lib.moe_linear_get_status.argtypes = [_P]
 _lib.moe_linear_get_status.restype = _I
 for _fn in ("moe_route_scored", "moe_route_scored_backward", "moe_layer_forward_scored",
@@ -627,8 +629,17 @@ def linear_debug(cg=0, bn=0, s=1, sw=1, timeout_us=0, withhold=False):
 
 def linear_get_status(stream=None) -> int:
     """Whether a bounded wait of linear or linear_backward ran out on the current device
-    since the last call of this (MOE_OK or MOE_ERR_TIMEOUT); syncs."""
+    since this thread's last call of this (MOE_OK or MOE_ERR_TIMEOUT); syncs."""
     return int(_lib.moe_linear_get_status(_stream(stream)))
+
+
+def linear_timeouts(stream=None) -> int:
+    """How many thread blocks of linear and linear_backward have given up a bounded wait on
+    the current device so far; syncs.  Callers that compare it with a count of their own
+    do not depend on who else asks."""
+    n = ctypes.c_uint32()
+    _check(_lib.moe_linear_timeouts(_stream(stream), ctypes.byref(n)), "moe_linear_timeouts")
+    return int(n.value)
 
 
 def _router_args(E, device, score, bias, n_groups, topk_groups, group_score, renorm, scale) -> RouterArgs:

@@ -389,9 +389,13 @@ typedef struct {
 moe_status moe_linear_debug_set(const moe_linear_debug* d);
 
 /* Synchronises `stream`, then tells whether a bounded wait (2 s) of any moe_linear or
- * moe_linear_backward on the current device ran out since the last call of this
- * (MOE_ERR_TIMEOUT: those outputs are not to be used). */
+ * moe_linear_backward on the current device, by any caller, ran out since the calling
+ * thread's last call of this, or ever (MOE_ERR_TIMEOUT: those outputs are not to be used). */
 moe_status moe_linear_get_status(void* stream);
+
+/* The count behind it, for callers that keep their own: how many thread blocks have given
+ * up such a wait on the current device since the library was loaded.  Synchronises. */
+moe_status moe_linear_timeouts(void* stream, uint32_t* count);
 
 /* ---- Expert parallelism: the fused return ---------------------------------
  * W ranks; rank o owns the local experts [o*El, (o+1)*El) of E = W*El.  Each

@@ -26,9 +26,11 @@ def test_a_withheld_operand_is_a_timeout_and_the_next_call_is_right(cg, bn, s, M
     with moe.linear_debug(cg, bn, s):
         want = moe.linear(x, W, out_dtype=dtype)
         assert moe.linear_get_status() == moe.MOE_OK
+        before = moe.linear_timeouts()
         with moe.linear_debug(cg, bn, s, timeout_us=LIMIT_US, withhold=True):
             moe.linear(x, W, out_dtype=dtype)
         assert moe.linear_get_status() == moe.MOE_ERR_TIMEOUT
+        assert moe.linear_timeouts() > before
         assert moe.linear_get_status() == moe.MOE_OK
     with moe.linear_debug(cg, bn, s):
         assert torch.equal(moe.linear(x, W, out_dtype=dtype), want)
@@ -47,6 +49,30 @@ def test_a_withheld_operand_of_slices(cg, sw):
     with moe.linear_debug(cg, 64, 1, sw):
         assert torch.equal(f(), want)
     assert moe.linear_get_status() == moe.MOE_OK
+
+
+def test_one_thread_does_not_clear_what_another_has_not_seen():
+    x, W = _rand(1, 300, 512), _rand(2, 512, 520)
+    assert moe.linear_get_status() in (moe.MOE_OK, moe.MOE_ERR_TIMEOUT)   # what came before
+    seen = []
+
+    def other(go, done):
+        seen.append(moe.linear_get_status())              # whatever there was before
+        done.set()
+        go.wait()
+        seen.append(moe.linear_get_status())
+        seen.append(moe.linear_get_status())
+
+    go, done = threading.Event(), threading.Event()
+    t = threading.Thread(target=other, args=(go, done))
+    t.start()
+    done.wait()
+    with moe.linear_debug(timeout_us=LIMIT_US, withhold=True):
+        moe.linear(x, W)
+    assert moe.linear_get_status() == moe.MOE_ERR_TIMEOUT and moe.linear_get_status() == moe.MOE_OK
+    go.set()
+    t.join()
+    assert seen[1:] == [moe.MOE_ERR_TIMEOUT, moe.MOE_OK]
 
 
 def test_settings_are_the_threads_own():
