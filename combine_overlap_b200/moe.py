@@ -763,6 +763,22 @@ class MoELayer:
         self.max_tokens = max_tokens
         self.router = router
         self.ws = alloc_workspace(max_tokens, self.d, self.f, self.E, k, W1.device)
+        self._timeouts = self._linear_timeouts() if router is not None else 0
+
+    def _linear_timeouts(self, stream=None) -> int:
+        with torch.cuda.device(self.ws.device):
+            return linear_timeouts(stream)
+
+    def get_status(self, stream=None):
+        """get_status of the layer's last call, and with a Router of its gate projection and
+        gradients too: MOE_ERR_TIMEOUT if a bounded wait of the layer's last call, or since the
+        last call of this of any linear or linear_backward on the device, ran out.  Syncs."""
+        code, consumers, bands = get_status(self.ws, stream)
+        if self.router is not None:
+            before, self._timeouts = self._timeouts, self._linear_timeouts(stream)
+            if code == MOE_OK and self._timeouts != before:
+                code = MOE_ERR_TIMEOUT
+        return code, consumers, bands
 
     def forward(self, x, logits=None, mode=MODE_OVERLAPPED, **kw):
         if x.shape[0] > self.max_tokens:
