@@ -702,7 +702,7 @@ def route_scored_backward(dgate, logits, topk_idx, score=SCORE_SOFTMAX, renorm=T
 def combine_backward(dout, y, row_of, topk_gate, want_dy=True, dy=None, stream=None):
     """The gradient of combine (moe_combine_backward): dout [T][d] bf16 -> (dy [T*k][d]
     bf16 or None, dgate [T][k] fp32).  A row_of of -1 is a dropped slot (dgate 0); rows of
-    dy that no slot names are left as they were (uninitialised, if dy is allocated here)."""
+    dy that no slot names are left as they were, and 0 in a dy that is made here."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return combine_backward(dout, y, row_of, topk_gate, want_dy, dy)
@@ -714,7 +714,7 @@ def combine_backward(dout, y, row_of, topk_gate, want_dy=True, dy=None, stream=N
     if dy is not None:
         _given(dy, _BF16, (T * k, d), "dy")
     elif want_dy:
-        dy = torch.empty_like(y)
+        dy = torch.zeros_like(y)
     dgate = torch.empty_like(topk_gate)
     st = _same_device((dout, "dout"), (y, "y"), (row_of, "row_of"), (topk_gate, "topk_gate"), (dy, "dy"))
     r = _lib.moe_combine_backward(o_ptr, y_ptr, r_ptr, topk_gate.data_ptr(), T, d, k,
@@ -807,7 +807,9 @@ class MoELayer:
         of dWg, dbg (fp32; dbg None without bg), dx (the gate projection's share, bf16),
         dlogits, and with want_dy dy [T*k][d], the gradient of the experts' outputs."""
         r = self.router
-        dy, dgate = combine_backward(dout, saved["y"], saved["row_of"], saved["gate"], want_dy=want_dy)
+        # forward_train drops no slot, so every row of dy is written
+        dy = torch.empty_like(saved["y"]) if want_dy else None
+        dy, dgate = combine_backward(dout, saved["y"], saved["row_of"], saved["gate"], want_dy=want_dy, dy=dy)
         dlogits = r.backward(dgate, saved["logits"], saved["idx"])
         dx, dWg, dbg = linear_backward(dlogits, saved["x"], r.Wg, want_dbias=r.bg is not None)
         return dict(dWg=dWg, dbg=dbg, dx=dx, dlogits=dlogits, dy=dy)
