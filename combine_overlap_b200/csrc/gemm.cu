@@ -1,7 +1,8 @@
 // gemm.cu -- the linear layer's products on the 5th-generation tensor cores: TMA tiles
 // into a ring of shared-memory stages, tcgen05 MMAs (bf16, fp32 accumulators in TMEM)
-// issued by one thread, and an epilogue (bias, activation, residual, one rounding) that
-// runs beside the next tile's main loop: two accumulators of up to 256 columns.
+// issued by one warp (a lane of it elected), and an epilogue (bias, activation, residual,
+// one rounding) that runs beside the next tile's main loop: two accumulators of up to 256
+// columns.
 //
 // Tiles and splits:
 //   CG = 1  a CTA per 128 x BN tile;
@@ -24,6 +25,7 @@
 // length run in kernels without the sums.
 #include "gemm.cuh"
 
+#include <limits.h>
 #include <string.h>
 
 namespace moe {
@@ -66,6 +68,7 @@ struct GemmArgs {
   int PB;                                 // planes of B
   int nst, stage_bytes;                   // ring
   int kps;                                // k-blocks of 64 per stage
+  int nkb, turn;                          // k-blocks of 64; those of A's first plane, where it has two (kps = 1)
   int b_bytes;                            // a stage's bytes of one plane of one CTA's B tile
   int b_boxes;                            // B, n contiguous: 64-column atoms per CTA and plane
   int a_whole, b_whole;                   // one copy brings all of a stage's A (B)
@@ -503,7 +506,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
   const uint32_t tmem = ctl->tmem_base;
   pdl_wait();
 
-  const int nkb = cdiv(a.K, 64);
+  const int nkb = a.nkb;
   const int t0 = blockIdx.x / (S * CG), tstep = gridDim.x / (S * CG);
   const int ntiles = a.tiles_m * a.tiles_n, units = ntiles * a.SW;
   // unit t: tile t % ntiles, slice t / ntiles; its k-blocks: as even as can be
@@ -522,7 +525,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
     bool ok = !(a.withhold && blockIdx.x == 0);
     const int kps = keep(a.kps), nst = keep(a.nst), PB = keep(a.PB), boxes = keep(a.b_boxes);
     const int b_bytes = keep(a.b_bytes), stage_bytes = keep(a.stage_bytes);
-    const int a_whole = keep(a.a_whole), b_whole = keep(a.b_whole);
+    const int a_whole = keep(a.a_whole), b_whole = keep(a.b_whole), turn = keep(a.turn);
     uint8_t* const ring = keep(smem);
     const CUtensorMap *ma = keep(&tm_a), *mb = keep(&tm_b);
     for (int t = t0; t < units && ok; t += tstep) {
@@ -540,7 +543,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
             else tma_load_4d(d, m, fb, x, y, z, p);
           };
           uint8_t* d = ring + stage * stage_bytes;
-          const int k = kb * 64;
+          const int ap = !AMN && !BMN && kb >= turn, kk = ap ? kb - turn : kb, k = kk * 64;
           if constexpr (AMN) {
             if (a_whole) {
               load(d, ma, 0, k, m0 >> 6, 0);
@@ -549,9 +552,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
               load(d + kps * 8192, ma, m0 + 64, k, 0, 0);
             }
           } else {
-            if (a_whole) load(d, ma, 0, m0, kb, 0);
+            if (a_whole) load(d, ma, 0, m0, kk, ap);
             else
-              for (int i = 0; i < kps; ++i) load(d + i * A_BYTES, ma, k + i * 64, m0, 0, 0);
+              for (int i = 0; i < kps; ++i) load(d + i * A_BYTES, ma, k + i * 64, m0, 0, ap);
           }
           d += kps * A_BYTES;
           if constexpr (BMN) {
@@ -560,7 +563,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
               for (int p = 0; p < PB; ++p)
                 for (int j = 0; j < boxes; ++j, d += kps * 8192) load(d, mb, n0 + j * 64, k, 0, p);
           } else {
-            if (b_whole) load(d, mb, 0, n0, kb, 0);
+            if (b_whole) load(d, mb, 0, n0, kk, 0);
             else
               for (int i = 0, step = b_bytes / kps; i < kps; ++i, d += step) load(d, mb, k + i * 64, n0, 0, 0);
           }
@@ -896,10 +899,7 @@ cudaError_t run_sums(const GemmProblem& p, const CUtensorMap (&m)[4], const Gemm
   return promo ? run_major<CG, 4, false>(p, m, a, grid, dev, s) : run_major<CG, 0, false>(p, m, a, grid, dev, s);
 }
 
-// SM cycles of one tile configuration, from rates measured on one B200: an MMA of
-// 128 (per CTA) x BN x 16 takes BN / 2 cycles, and a stage's bytes arrive at no more than
-// FILL per cycle and SM; a tile's epilogue is hidden but for the last, and a pair's two
-// CTAs cost a tile some cycles to keep in step.
+// A product's tiles and the splits of its reduction.
 struct Shape { int CG, BN, S, SW; };
 
 // Clusters of `size` CTAs that a device holds at once (one CTA per SM): fewer than SMs /
@@ -930,8 +930,13 @@ int clusters_of(int dev, int nsm, int size) {
   return most[dev][size];
 }
 
+// SM cycles of one tile configuration, from rates measured on one B200: an MMA of
+// 128 (per CTA) x BN x 16 takes BN / 2 cycles, and a stage's bytes arrive at no more than
+// FILL per cycle and SM; a tile's epilogue is hidden but for the last, and a pair's two
+// CTAs cost a tile some cycles to keep in step.  (Four k-blocks per tile, dx of 16384 x 4096
+// over 128 in two terms: 52 us in single blocks, 56 in pairs; eight of them: 82 and 76.)
 double cost(const GemmProblem& p, int dev, int nsm, Shape c) {
-  const int nkb = cdiv(p.K, 64), units = cdiv(p.M, 128 * c.CG) * cdiv(p.N, c.BN) * c.SW;
+  const int nkb = cdiv(p.K, 64) * p.A.planes, units = cdiv(p.M, 128 * c.CG) * cdiv(p.N, c.BN) * c.SW;
   const int cols = c.BN / c.CG, P = p.B.planes;
   // per k-block: the MMAs; shared memory's 128 bytes per cycle for the tiles' way in and
   // the MMAs' operands; the way from L2
@@ -942,7 +947,7 @@ double cost(const GemmProblem& p, int dev, int nsm, Shape c) {
   double tail = 2500.0 + 8.0 * c.BN + (c.CG > 1 ? 800.0 : 0.0);
   if (c.S > 1) tail += 2500.0 + 16.0 * c.BN;
   if (c.SW > 1) tail += 3500.0 + c.SW * (double)p.M * p.N * 8.0 / (nsm * 40.0);
-  return waves * (cdiv(nkb, c.S * c.SW) * kb + (c.CG > 1 ? 1500.0 : 300.0)) + tail;
+  return waves * (cdiv(nkb, c.S * c.SW) * kb + (c.CG > 1 ? 1800.0 : 300.0)) + tail;
 }
 
 // BN is a multiple of 32, so that a chunk of the epilogue lies in one tile, or 16 for N <= 16.
@@ -953,7 +958,7 @@ Shape pick(const GemmProblem& p, int dev, int nsm) {
     const double t = cost(p, dev, nsm, c);
     if (t < least) { least = t; best = c; }
   };
-  const int nkb = cdiv(p.K, 64), most = min(p.B.planes > 1 ? 128 : 256, cdiv(p.N, 32) * 32);
+  const int nkb = cdiv(p.K, 64) * p.A.planes, most = min(p.B.planes > 1 ? 128 : 256, cdiv(p.N, 32) * 32);
   const int slices = p.ws ? gemm_slices(p.M, p.N) : 1;
   for (int CG = 1; CG <= (p.M > 128 ? 2 : 1); ++CG) {
     const int rows = cdiv(p.M, 128 * CG), fit = clusters_of(dev, nsm, CG);
@@ -979,7 +984,7 @@ Shape pick(const GemmProblem& p, int dev, int nsm) {
 
 // Whether a shape given by gemm_debug is one that pick() may come to for some size.
 bool legal(const GemmProblem& p, int dev, int nsm, Shape c) {
-  const int nkb = cdiv(p.K, 64), slices = p.ws ? gemm_slices(p.M, p.N) : 1;
+  const int nkb = cdiv(p.K, 64) * p.A.planes, slices = p.ws ? gemm_slices(p.M, p.N) : 1;
   if (c.CG < 1 || c.CG > 2 || (c.CG == 2 && p.M <= 128)) return false;
   if (c.BN != 16 && (c.BN < 32 || c.BN % 32 != 0 || c.BN > min(p.B.planes > 1 ? 128 : 256, cdiv(p.N, 32) * 32))) return false;
   if (c.BN == 16 && (c.CG == 2 || p.N > 16)) return false;
@@ -1086,6 +1091,13 @@ cudaError_t launch_gemm(const GemmProblem& p, cudaStream_t s) {
   GemmArgs a;
   memset(&a, 0, sizeof(a));
   a.M = p.M; a.N = p.N; a.K = p.K;
+  a.nkb = cdiv(p.K, 64) * p.A.planes;
+  a.turn = INT_MAX;
+  if (p.A.planes > 1) {
+    if (p.A.planes > 2 || p.a_mn || p.b_mn) return cudaErrorInvalidValue;
+    a.turn = cdiv(p.K, 64);
+    a.K = INT_MAX;                        // a plane's last k-block is multiplied whole, with TMA's zeros
+  }
   a.PB = p.B.planes;
   a.ep = p.ep;
   a.limit = gemm_debug.limit;
@@ -1102,7 +1114,7 @@ cudaError_t launch_gemm(const GemmProblem& p, cudaStream_t s) {
   a.b_boxes = cdiv(cols, 64);
   const int b_kb = p.b_mn ? a.b_boxes * 8192 : cols * 128;   // one k-block of one plane
   // the ring's tiles start on 1024-byte boundaries (cols is a multiple of 16)
-  a.kps = A_BYTES + a.PB * b_kb <= 24576 ? 2 : 1;
+  a.kps = A_BYTES + a.PB * b_kb <= 24576 && p.A.planes == 1 ? 2 : 1;
   a.b_bytes = a.kps * b_kb;
   a.stage_bytes = a.kps * A_BYTES + a.PB * a.b_bytes;
   a.a_whole = (p.a_mn ? p.M : p.K) % 64 == 0;
@@ -1111,7 +1123,7 @@ cudaError_t launch_gemm(const GemmProblem& p, cudaStream_t s) {
   a.group = c.CG == 2 ? 8 : 16;
   const bool f32 = p.ep.out_f32 || a.SW > 1;
   a.chunk = p.ep.out_f32 ? CHAIN_F32 : CHAIN_BF16;
-  const bool promo = cdiv(cdiv(p.K, 64), a.S * a.SW) > a.chunk;
+  const bool promo = cdiv(a.nkb, a.S * a.SW) > a.chunk;
   CUtensorMap m[4];
   if (!(p.a_mn ? encode4(&m[0], p.A, p.M, p.K, 64 * a.kps, a.a_whole, 2, 1)
                : encode4(&m[0], p.A, p.K, p.M, 128, a.a_whole, a.kps, 1)) ||

@@ -5,13 +5,15 @@
 
 namespace moe {
 
-// C [M][N] = epilogue( sum over B's planes p and over k of A(m, k) B_p(k, n) ).
+// C [M][N] = epilogue( sum over planes p and over k of A_p(m, k) B_p(k, n) ), an operand of one
+// plane standing in for all of them.
 // An operand is `planes` bf16 matrices, `plane` bytes apart, of rows `ld` bytes apart
 // (multiples of 16; base 16-byte aligned):
-//   A: [M][K] (k contiguous) or, a_mn set, [K][M] (m contiguous); its first plane counts
+//   A: [M][K] (k contiguous) or, a_mn set, [K][M] (m contiguous; one plane)
 //   B: [K][N] (n contiguous, b_mn set) or [N][K] (k contiguous; one plane)
-// Planes are the bf16 terms of an operand of more than 8 bits; each stage of the
-// operand ring holds all of them, so A is read once for all.
+// Planes are the bf16 terms of an operand of more than 8 bits.  Each stage of the operand ring
+// holds all of B's, so A is read once for all; A's (two at the most, with both k contiguous)
+// follow one another as a longer reduction.
 struct GemmOperand {
   const void* p;
   size_t ld, plane;

@@ -210,10 +210,12 @@ int dact_rows(int M, int N) {
   return (long long)cdiv(M, 64) * cdiv(N, 128) >= 600 ? max(64, most) : most;
 }
 
-// The bf16 terms that du goes in as.  bf16 gradients take it rounded once, as a stored
-// bf16 gradient would be: an error of the size of their own rounding.  An fp32 dW takes
-// three terms, all 24 bits.  dout in bf16 without an activation is du itself.
-int terms_of(const LinearBwdArgs& a) { return (a.dout_f32 || a.act) && a.dW && a.dW_f32 ? 3 : 1; }
+// The bf16 terms that du is kept as.  With dW in bf16 it is rounded once, as a stored bf16
+// gradient would be: an error of the size of the gradients' own rounding.  An fp32 dW takes
+// three terms, all 24 bits, and dx beside it the first two: 16 bits, far below the rounding of a
+// bf16 dx.  Whether dW is wanted in this call changes no bit of the others.  dout in bf16
+// without an activation is du itself.
+int terms_of(const LinearBwdArgs& a) { return !(a.dout_f32 || a.act) || !a.dW_f32 ? 1 : a.dW ? 3 : 2; }
 
 }  // namespace
 
@@ -272,7 +274,7 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, void* ws, cudaStream_t s) 
   if (!direct || a.dbias) {
     float* sums = !a.dbias ? nullptr : nblk == 1 ? a.dbias : part;
     __nv_bfloat16* to = (__nv_bfloat16*)du.p;
-    const int n = direct ? 0 : terms;
+    const int n = direct || !(a.dx || a.dW) ? 0 : terms;   // 0: for dbias alone
     switch (a.act * 2 + (terms > 1)) {
       case 0: case 1: e = launch_dact<0, false>(a, rows, n, to, n8, sums, s); break;
       case 2: case 3: e = launch_dact<1, false>(a, rows, n, to, n8, sums, s); break;
@@ -288,7 +290,7 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, void* ws, cudaStream_t s) 
   if (a.dx) {
     GemmProblem p = {};
     p.A = du;
-    p.A.planes = 1;
+    p.A.planes = min(terms, 2);
     p.B = W;
     p.M = a.M; p.N = a.K; p.K = a.N;
     p.ep.out = a.dx;

@@ -576,7 +576,8 @@ def linear_backward(dout, x, W, pre=None, act=ACT_NONE, dW_dtype=torch.float32, 
                     want_dbias=False, ws=None, stream=None):
     """The gradients of linear (moe_linear_backward): dout [M][N] bf16 or fp32 ->
     (dx [M][K] bf16, dW [K][N] of dW_dtype, dbias [N] fp32), None where not wanted.
-    The residual's gradient is dout itself.  pre: linear's second result, with an
+    dW_dtype float32 also keeps 16 bits of the pre-activation's gradient for dx, bfloat16
+    8.  The residual's gradient is dout itself.  pre: linear's second result, with an
     activation.  ws: linear_backward_workspace_size(M, K, N) bytes (None: allocated here)."""
     if stream is not None:
         with torch.cuda.stream(stream):

@@ -350,9 +350,11 @@ moe_status moe_linear(const moe_linear_args* args, void* ws, size_t ws_bytes, vo
 /* The gradients:  du = dout * act'(pre),
  *   dx = du W^T,   dW = x^T du,   dbias = sum_m du      (d residual is dout itself).
  * Each output is optional.  pre is read with an activation only.  dout is bf16 or
- * fp32.  The products run on bf16 operands: for a dW in fp32, du goes in as a sum of three
- * bf16 terms, which hold all 24 bits; for bf16 gradients it is rounded to bf16 once, as a
- * stored activation gradient would be.  Without an activation a bf16 dout is du, exactly. */
+ * fp32.  The products run on bf16 operands.  With dW_dtype fp32, du goes into dW as a sum of
+ * three bf16 terms, which hold all 24 bits, and into dx as two, 16 bits; with dW_dtype bf16 it
+ * is rounded to bf16 once for both, as a stored activation gradient would be (dx with dW NULL
+ * goes by dW_dtype, too).  Without an activation a bf16 dout is du, exactly.  An infinity in x
+ * or W meets terms of both signs and may come out as a NaN. */
 typedef struct {
   int M, K, N;
   const void* dout;         /* [M][N] of dout_dtype                                  */
@@ -361,7 +363,7 @@ typedef struct {
   const void* pre;          /* [M][N] bf16, with an activation                       */
   int act;                  /* moe_act                                               */
   int dout_dtype;           /* moe_dtype                                             */
-  int dW_dtype;             /* moe_dtype                                             */
+  int dW_dtype;             /* moe_dtype; also says in how many bits du is kept      */
   void* dx;                 /* [M][K] bf16, or NULL                                  */
   void* dW;                 /* [K][N] of dW_dtype, or NULL                           */
   float* dbias;             /* [N] fp32, or NULL                                     */
