@@ -194,10 +194,9 @@ __device__ __forceinline__ uint32_t choose_groups(const Plan& o, int lane, U min
   return chosen;
 }
 
-// The value of each group, as an ordered key in the lane that speaks for it (lane g << shift
-// for group g), 0 elsewhere.  v: what the groups compare, of this lane's live experts.
+// The two largest values seen, a >= b.
 template <typename F>
-struct Two {                                      // the two largest, a >= b
+struct Two {
   F a, b;
   __device__ __forceinline__ void add(F v) {
     const F low = a < v ? a : v;
@@ -215,6 +214,8 @@ struct Two {                                      // the two largest, a >= b
   }
 };
 
+// The value of each group, as an ordered key in the lane that speaks for it (lane g << shift
+// for group g), 0 elsewhere.  v: what the groups compare, of this lane's live experts.
 template <typename U, typename F, int CM>
 __device__ __forceinline__ U group_values(const Plan& o, int lane, const F (&v)[CM], uint32_t live, Two<F>* seen) {
   Two<F> t = {-INFINITY, -INFINITY};
