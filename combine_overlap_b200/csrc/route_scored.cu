@@ -590,8 +590,8 @@ route_scored_kernel(const float* __restrict__ logits, int T, int E, int k, const
 //   sigmoid: dz_e = c_e p_e (1 - p_e);
 //   with renorm and the shares q_j = w_j / S: dz_e = q_e (c_e - sum_j q_j c_j), for the sigmoid
 //   times 1 - p_e.  The softmax's own normaliser cancels, and dz is 0 beside the chosen.
-// Shares, not scores over S^2: 1 / S overflows where the chosen scores are below 2^-1024, and
-// where one expert has the whole sum its share is 1 and the gradient exactly 0.
+// Shares, not scores over S^2: 1 / S overflows where the chosen scores are below 2^-1024.
+// Where one expert has the whole sum the gradient is exactly 0.
 // A warp takes 4 tokens: lane 8 q + j is token q's slot j, in 64 bits; then the warp
 // writes the 4 rows, and the slots their experts' values over them.  `zero`: there is
 // nothing beside the chosen.
@@ -609,10 +609,11 @@ route_scored_bwd_kernel(const float* __restrict__ dgate, const float* __restrict
   const bool slot = j < k && t < T;
   int e = slot ? topk_idx[(size_t)t * k + j] : -1;
   if ((unsigned)e >= (unsigned)E) e = -1;
+  const float dg = slot ? __ldg(dgate + (size_t)t * k + j) : 0.0f;   // on its way beside the chain of id and logit
   const float z = e >= 0 ? __ldg(logits + (size_t)t * E + e) : -INFINITY;
   const bool live = z >= -FLT_MAX;
   // a masked expert's gate is the constant 0: what its dgate holds, NaN or not, counts for nothing
-  const double c = live ? (double)o.scale * (double)dgate[(size_t)t * k + j] : 0.0;
+  const double c = live ? (double)o.scale * (double)dg : 0.0;
   const double zd = (double)fminf(z, FLT_MAX);
   const bool zero = o.score != 0 || o.renorm;
   float my_top = 0.0f, my_sum = 1.0f;
@@ -638,12 +639,13 @@ route_scored_bwd_kernel(const float* __restrict__ dgate, const float* __restrict
     w = live ? 1.0 / (1.0 + x) : 0.0;
     rest = w < 0.5 ? 1.0 - w : x * w;
   }
-  double share = w;
+  double share = w, dot = 0.0;
+  if (o.score == 0 || o.renorm) dot = sum8(c * w);
   if (o.renorm) {
     const double S = sum8(w);
-    share = S > 0.0 ? w / S : 0.0;
+    dot = S > 0.0 ? dot / S : 0.0;
+    share = w < S ? w / S : 0.0;                  // w = S: the share is 1, the difference 0
   }
-  const double dot = o.score == 0 || o.renorm ? sum8(share * c) : 0.0;
   const float dz = live ? (float)(share * (c - dot) * rest) : 0.0f;
   if (zero) {
     // 4 rows of zeros in one run
