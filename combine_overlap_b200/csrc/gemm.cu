@@ -65,10 +65,9 @@ struct GemmArgs {
   int tiles_m, tiles_n;
   int BN;                                 // columns per tile, a multiple of 16, <= 256
   int S, SW;                              // split of the reduction: in a cluster, in slices
-  int PB;                                 // planes of B
+  int PA, PB;                             // planes
   int nst, stage_bytes;                   // ring
-  int kps;                                // k-blocks of 64 per stage
-  int nkb, turn;                          // k-blocks of 64; those of A's first plane, where it has two (kps = 1)
+  int kps;                                // k-blocks of 64 per stage; 1 with two planes of A
   int b_bytes;                            // a stage's bytes of one plane of one CTA's B tile
   int b_boxes;                            // B, n contiguous: 64-column atoms per CTA and plane
   int a_whole, b_whole;                   // one copy brings all of a stage's A (B)
@@ -506,7 +505,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
   const uint32_t tmem = ctl->tmem_base;
   pdl_wait();
 
-  const int nkb = a.nkb;
+  const int nkb = cdiv(a.K, 64);
   const int t0 = blockIdx.x / (S * CG), tstep = gridDim.x / (S * CG);
   const int ntiles = a.tiles_m * a.tiles_n, units = ntiles * a.SW;
   // unit t: tile t % ntiles, slice t / ntiles; its k-blocks: as even as can be
@@ -525,7 +524,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
     bool ok = !(a.withhold && blockIdx.x == 0);
     const int kps = keep(a.kps), nst = keep(a.nst), PB = keep(a.PB), boxes = keep(a.b_boxes);
     const int b_bytes = keep(a.b_bytes), stage_bytes = keep(a.stage_bytes);
-    const int a_whole = keep(a.a_whole), b_whole = keep(a.b_whole), turn = keep(a.turn);
+    const int a_whole = keep(a.a_whole), b_whole = keep(a.b_whole), PA = keep(a.PA);
     uint8_t* const ring = keep(smem);
     const CUtensorMap *ma = keep(&tm_a), *mb = keep(&tm_b);
     for (int t = t0; t < units && ok; t += tstep) {
@@ -543,7 +542,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
             else tma_load_4d(d, m, fb, x, y, z, p);
           };
           uint8_t* d = ring + stage * stage_bytes;
-          const int ap = !AMN && !BMN && kb >= turn, kk = ap ? kb - turn : kb, k = kk * 64;
+          const int k = kb * 64;
           if constexpr (AMN) {
             if (a_whole) {
               load(d, ma, 0, k, m0 >> 6, 0);
@@ -552,18 +551,20 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
               load(d + kps * 8192, ma, m0 + 64, k, 0, 0);
             }
           } else {
-            if (a_whole) load(d, ma, 0, m0, kk, ap);
+            if (a_whole) load(d, ma, 0, m0, kb, 0);
+            else if (PA > 1)
+              for (int p = 0; p < PA; ++p) load(d + p * A_BYTES, ma, k, m0, 0, p);
             else
-              for (int i = 0; i < kps; ++i) load(d + i * A_BYTES, ma, k + i * 64, m0, 0, ap);
+              for (int i = 0; i < kps; ++i) load(d + i * A_BYTES, ma, k + i * 64, m0, 0, 0);
           }
-          d += kps * A_BYTES;
+          d += kps * PA * A_BYTES;
           if constexpr (BMN) {
             if (b_whole) load(d, mb, 0, k, n0 >> 6, 0);
             else
               for (int p = 0; p < PB; ++p)
                 for (int j = 0; j < boxes; ++j, d += kps * 8192) load(d, mb, n0 + j * 64, k, 0, p);
           } else {
-            if (b_whole) load(d, mb, 0, n0, kk, 0);
+            if (b_whole) load(d, mb, 0, n0, kb, 0);
             else
               for (int i = 0, step = b_bytes / kps; i < kps; ++i, d += step) load(d, mb, k + i * 64, n0, 0, 0);
           }
@@ -587,15 +588,17 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
       if (CG == 2) tc_commit_pair(bar, mask);
       else tc_commit(bar);
     };
-    const int kps = keep(a.kps), nst = keep(a.nst), PB = keep(a.PB), chunk = keep(a.chunk), K = keep(a.K);
+    const int kps = keep(a.kps), nst = keep(a.nst), PB = keep(a.PB), chunk = keep(a.chunk);
+    // two planes of A are multiplied as two k-blocks of one B, the last k-block whole (TMA's zeros)
+    const int PA = keep(a.PA), K = keep(PA > 1 ? INT_MAX : a.K);
     // Descriptors of the first stage.  16 of k further on: 32 bytes in a K-major row, 16 rows
     // of 128 bytes otherwise; the next k-block: the next tile, or 64 rows (the address field
     // is in units of 16 bytes)
     constexpr uint64_t KA = AMN ? 128 : 2, KB = BMN ? 128 : 2;
     const uint64_t ad0 = smem_desc_sw128(smem_u32(smem), AMN ? kps * 8192 : 16, 1024);
-    const uint64_t bd0 = smem_desc_sw128(smem_u32(smem) + kps * A_BYTES, BMN ? kps * 8192 : 16, 1024);
+    const uint64_t bd0 = smem_desc_sw128(smem_u32(smem) + kps * PA * A_BYTES, BMN ? kps * 8192 : 16, 1024);
     const int stage16 = keep(a.stage_bytes >> 4), b16 = keep(a.b_bytes >> 4);
-    const int xkb = AMN ? 512 : A_BYTES >> 4, ykb = keep(BMN ? 512 : (a.b_bytes / a.kps) >> 4);
+    const int xkb = AMN ? 512 : A_BYTES >> 4, ykb = keep(BMN ? 512 : PA > 1 ? 0 : (a.b_bytes / a.kps) >> 4);
     int stage = 0, acc = 0;
     uint32_t ph = 0, aph = 0;
     bool ok = true;
@@ -607,7 +610,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
         if (!g_wait<CG>(&ctl->full[stage], ph, ctl)) { ok = false; break; }
         tc_fence_after();
         const uint32_t dt = tmem + (uint32_t)(acc * ACC_COLS);
-        const int n = min(kps, kb1 - kb);
+        const int n = PA > 1 ? PA : min(kps, kb1 - kb);
         const uint32_t more = in ? 1u : 0u;
         in += kps;
         const bool end = in == chunk || kb + kps >= kb1;
@@ -936,11 +939,11 @@ int clusters_of(int dev, int nsm, int size) {
 // CTAs cost a tile some cycles to keep in step.  (Four k-blocks per tile, dx of 16384 x 4096
 // over 128 in two terms: 52 us in single blocks, 56 in pairs; eight of them: 82 and 76.)
 double cost(const GemmProblem& p, int dev, int nsm, Shape c) {
-  const int nkb = cdiv(p.K, 64) * p.A.planes, units = cdiv(p.M, 128 * c.CG) * cdiv(p.N, c.BN) * c.SW;
-  const int cols = c.BN / c.CG, P = p.B.planes;
+  const int nkb = cdiv(p.K, 64), units = cdiv(p.M, 128 * c.CG) * cdiv(p.N, c.BN) * c.SW;
+  const int cols = c.BN / c.CG, P = p.B.planes * p.A.planes;
   // per k-block: the MMAs; shared memory's 128 bytes per cycle for the tiles' way in and
   // the MMAs' operands; the way from L2
-  const double in = 16384.0 + p.B.planes * (p.b_mn ? cdiv(cols, 64) * 8192.0 : cols * 128.0);
+  const double in = 16384.0 * p.A.planes + p.B.planes * (p.b_mn ? cdiv(cols, 64) * 8192.0 : cols * 128.0);
   const double mma = max(2.0 * c.BN * P, (in + P * (16384.0 + cols * 128.0)) / 128.0);
   const double kb = max(max(mma, in / G_FILL), 150.0);
   const int waves = cdiv(units, clusters_of(dev, nsm, c.CG * c.S));
@@ -958,7 +961,7 @@ Shape pick(const GemmProblem& p, int dev, int nsm) {
     const double t = cost(p, dev, nsm, c);
     if (t < least) { least = t; best = c; }
   };
-  const int nkb = cdiv(p.K, 64) * p.A.planes, most = min(p.B.planes > 1 ? 128 : 256, cdiv(p.N, 32) * 32);
+  const int nkb = cdiv(p.K, 64), most = min(p.B.planes > 1 ? 128 : 256, cdiv(p.N, 32) * 32);
   const int slices = p.ws ? gemm_slices(p.M, p.N) : 1;
   for (int CG = 1; CG <= (p.M > 128 ? 2 : 1); ++CG) {
     const int rows = cdiv(p.M, 128 * CG), fit = clusters_of(dev, nsm, CG);
@@ -984,7 +987,7 @@ Shape pick(const GemmProblem& p, int dev, int nsm) {
 
 // Whether a shape given by gemm_debug is one that pick() may come to for some size.
 bool legal(const GemmProblem& p, int dev, int nsm, Shape c) {
-  const int nkb = cdiv(p.K, 64) * p.A.planes, slices = p.ws ? gemm_slices(p.M, p.N) : 1;
+  const int nkb = cdiv(p.K, 64), slices = p.ws ? gemm_slices(p.M, p.N) : 1;
   if (c.CG < 1 || c.CG > 2 || (c.CG == 2 && p.M <= 128)) return false;
   if (c.BN != 16 && (c.BN < 32 || c.BN % 32 != 0 || c.BN > min(p.B.planes > 1 ? 128 : 256, cdiv(p.N, 32) * 32))) return false;
   if (c.BN == 16 && (c.CG == 2 || p.N > 16)) return false;
@@ -1091,14 +1094,9 @@ cudaError_t launch_gemm(const GemmProblem& p, cudaStream_t s) {
   GemmArgs a;
   memset(&a, 0, sizeof(a));
   a.M = p.M; a.N = p.N; a.K = p.K;
-  a.nkb = cdiv(p.K, 64) * p.A.planes;
-  a.turn = INT_MAX;
-  if (p.A.planes > 1) {
-    if (p.A.planes > 2 || p.a_mn || p.b_mn) return cudaErrorInvalidValue;
-    a.turn = cdiv(p.K, 64);
-    a.K = INT_MAX;                        // a plane's last k-block is multiplied whole, with TMA's zeros
-  }
+  a.PA = p.A.planes;
   a.PB = p.B.planes;
+  if (a.PA > 1 && (a.PA > 2 || p.a_mn || p.b_mn || a.PB > 1)) return cudaErrorInvalidValue;
   a.ep = p.ep;
   a.limit = gemm_debug.limit;
   a.withhold = gemm_debug.withhold;
@@ -1114,19 +1112,19 @@ cudaError_t launch_gemm(const GemmProblem& p, cudaStream_t s) {
   a.b_boxes = cdiv(cols, 64);
   const int b_kb = p.b_mn ? a.b_boxes * 8192 : cols * 128;   // one k-block of one plane
   // the ring's tiles start on 1024-byte boundaries (cols is a multiple of 16)
-  a.kps = A_BYTES + a.PB * b_kb <= 24576 && p.A.planes == 1 ? 2 : 1;
+  a.kps = a.PA == 1 && A_BYTES + a.PB * b_kb <= 24576 ? 2 : 1;
   a.b_bytes = a.kps * b_kb;
-  a.stage_bytes = a.kps * A_BYTES + a.PB * a.b_bytes;
+  a.stage_bytes = a.kps * a.PA * A_BYTES + a.PB * a.b_bytes;
   a.a_whole = (p.a_mn ? p.M : p.K) % 64 == 0;
   a.b_whole = p.b_mn ? p.N % 64 == 0 && cols % 64 == 0 : p.K % 64 == 0;
   a.nst = min(G_MAX_NST, G_RING / a.stage_bytes);
   a.group = c.CG == 2 ? 8 : 16;
   const bool f32 = p.ep.out_f32 || a.SW > 1;
-  a.chunk = p.ep.out_f32 ? CHAIN_F32 : CHAIN_BF16;
-  const bool promo = cdiv(a.nkb, a.S * a.SW) > a.chunk;
+  a.chunk = (p.ep.out_f32 ? CHAIN_F32 : CHAIN_BF16) / a.PA;
+  const bool promo = cdiv(cdiv(p.K, 64), a.S * a.SW) > a.chunk;
   CUtensorMap m[4];
   if (!(p.a_mn ? encode4(&m[0], p.A, p.M, p.K, 64 * a.kps, a.a_whole, 2, 1)
-               : encode4(&m[0], p.A, p.K, p.M, 128, a.a_whole, a.kps, 1)) ||
+               : encode4(&m[0], p.A, p.K, p.M, 128, a.a_whole, a.kps, a.PA)) ||
       !(p.b_mn ? encode4(&m[1], p.B, p.N, p.K, 64 * a.kps, a.b_whole, a.b_boxes, a.PB)
                : encode4(&m[1], p.B, p.K, p.N, cols, a.b_whole, a.kps, 1)))
     return cudaErrorInvalidValue;

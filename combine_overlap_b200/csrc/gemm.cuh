@@ -12,8 +12,8 @@ namespace moe {
 //   A: [M][K] (k contiguous) or, a_mn set, [K][M] (m contiguous; one plane)
 //   B: [K][N] (n contiguous, b_mn set) or [N][K] (k contiguous; one plane)
 // Planes are the bf16 terms of an operand of more than 8 bits.  Each stage of the operand ring
-// holds all of B's, so A is read once for all; A's (two at the most, with both k contiguous)
-// follow one another as a longer reduction.
+// holds all of them, so the other operand is read once for all.  A has two at the most, where k
+// is contiguous in both, and B then one.
 struct GemmOperand {
   const void* p;
   size_t ld, plane;
