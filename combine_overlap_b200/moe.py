@@ -764,7 +764,9 @@ class MoELayer:
         self.max_tokens = max_tokens
         self.router = router
         self.ws = alloc_workspace(max_tokens, self.d, self.f, self.E, k, W1.device)
-        self._timeouts = self._linear_timeouts() if router is not None else 0
+        self._timeouts = 0
+        if router is not None and not torch.cuda.is_current_stream_capturing():
+            self._timeouts = self._linear_timeouts()
 
     def _linear_timeouts(self, stream=None) -> int:
         with torch.cuda.device(self.ws.device):
